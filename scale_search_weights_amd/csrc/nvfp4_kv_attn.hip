@@ -24,9 +24,21 @@ namespace nvfp4 {
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef float f2 __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
+#ifndef WANT_ROWS
+#define WANT_ROWS 768
+#endif
+#ifndef WANT_TILE
+#define WANT_TILE 512
+#endif
+#ifndef TILE_NT
+#define TILE_NT 2
+#define TILE_OCC 2
+#endif
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Attn {
@@ -38,8 +50,11 @@ struct Attn {
   int64_t table_width;
   int tokens, heads, kv_heads, group, hd, page_shift, pages, max_q, max_len, causal;
   float scale;
-  int prefix;               // the job is the shared prefix: all tokens over one page list
-  int piece, pieces, row_tiles, slot0, direct;
+  int prefix;    // the job is the shared prefix: all tokens over one page list
+  int batch, row_tiles, slots;
+  float target;  // own tokens: pieces wanted in all; 0 for one piece a sequence
+  int piece;     // prefix: tokens of a piece
+  int direct;    // one piece a row, written straight to out
   void *out;
   float *lse, *opart;
   float2 *ml;
@@ -67,6 +82,90 @@ __device__ __forceinline__ Job job_of(const Attn &p, int b) {
     j.pages = p.table + b * p.table_width;
   }
   return j;
+}
+
+// The sequences' own tokens are cut into pieces of equal length, a multiple of 128 chosen from
+// the lengths found on the device so that about `target` pieces come out in all (at most
+// target + batch: every sequence may add one that is not full). Slots number the pieces over
+// all sequences, so the grid has few workgroups without work however unequal the lengths
+// are. Every wave finds its piece by itself: two passes over the lengths.
+struct Piece {
+  int b, first, count, tokens;  // sequence, its first slot, its pieces, tokens of a full piece
+};
+
+__device__ __forceinline__ int units_of(const int32_t *kv_lens, int b, int max_len) {
+  return (min(max(kv_lens[b], 0), max_len) + 127) >> 7;
+}
+
+__device__ __forceinline__ int piece_units(const int32_t *kv_lens, int batch, int max_len,
+                                           float target, int lane) {
+  float sum = 0.0f;
+  for (int b = lane; b < batch; b += 64) sum += (float)units_of(kv_lens, b, max_len);
+#pragma unroll
+  for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  const float x = ceilf(sum / target);  // the same in every wave: same order, same bits
+  return __builtin_amdgcn_readfirstlane(x < 1.0f ? 1 : (x > 8388608.0f ? 8388608 : (int)x));
+}
+
+// The piece of `slot`, or (want_b >= 0) the slots of sequence want_b. b = -1: no such piece.
+__device__ __forceinline__ Piece find_piece(const int32_t *kv_lens, int batch, int max_len,
+                                            float target, int slot, int want_b, int lane) {
+  const int per = piece_units(kv_lens, batch, max_len, target, lane);
+  Piece r = {-1, 0, 0, per << 7};
+  int before = 0;
+  for (int b0 = 0; b0 < batch; b0 += 64) {
+    const int b = b0 + lane;
+    const int n = b < batch ? (units_of(kv_lens, b, max_len) + per - 1) / per : 0;
+    int upto = n;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(upto, off, 64);
+      if (lane >= off) upto += o;
+    }
+    const bool mine = want_b >= 0 ? b == want_b
+                                  : slot >= before + upto - n && slot < before + upto;
+    const unsigned long long hit = __ballot(mine);
+    if (hit) {
+      const int at = __builtin_ctzll(hit);
+      r.b = b0 + at;
+      r.count = __builtin_amdgcn_readlane(n, at);
+      r.first = before + __builtin_amdgcn_readlane(upto, at) - r.count;
+      return r;
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return r;
+}
+
+// A workgroup's share of the call: a row tile of one key/value head, tokens t0 .. t1 - 1, and
+// where its rows go: row r of the job to partial row `part + r` unless direct.
+struct Share {
+  Job j;
+  int h, rt, t0, t1, direct;
+  int64_t part;
+};
+
+__device__ __forceinline__ bool share_of(const Attn &p, int lane, Share &s) {
+  int w = blockIdx.x;
+  const int slot = w % p.slots;
+  w /= p.slots;
+  s.h = w % p.kv_heads;
+  s.rt = w / p.kv_heads;
+  s.direct = p.direct;
+  if (p.prefix || p.target == 0.0f) {
+    s.j = job_of(p, p.prefix ? 0 : slot);
+    s.t0 = p.prefix ? slot * p.piece : 0;
+    s.t1 = p.prefix ? min(s.j.len, s.t0 + p.piece) : s.j.len;
+  } else {
+    const Piece x = find_piece(p.kv_lens, p.batch, p.max_len, p.target, slot, -1, lane);
+    if (x.b < 0) return false;
+    s.j = job_of(p, x.b);
+    s.t0 = (slot - x.first) * x.tokens;
+    s.t1 = min(s.j.len, s.t0 + x.tokens);
+  }
+  const int rows = p.prefix ? p.tokens * p.group : p.max_q * p.group;
+  s.part = ((int64_t)slot * p.kv_heads + s.h) * rows;
+  return true;
 }
 
 __device__ __forceinline__ h2 codes2(unsigned w, int b) {
@@ -229,10 +328,13 @@ template <int HD>
 __device__ __forceinline__ void value_frags(const Tile<HD> &x, int lane, const _Float16 *lds,
                                             int word, h8 *out) {
   const int i = lane & 15, quad = lane >> 4;
+  // the scales come from other lanes of the wave: order the reads after their writes
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
   const _Float16 *row = lds + ((i * (HD / 16)) >> 4) * kVsRow + 4 * quad;
-  union { uint2 w[2]; h2 s[4]; } sc;
-  sc.w[0] = *reinterpret_cast<const uint2 *>(row);
-  sc.w[1] = *reinterpret_cast<const uint2 *>(row + 16);
+  const h4 s0 = *reinterpret_cast<const h4 *>(row), s1 = *reinterpret_cast<const h4 *>(row + 16);
+  const h2 sc[4] = {{s0[0], s0[1]}, {s0[2], s0[3]}, {s1[0], s1[1]}, {s1[2], s1[3]}};
   constexpr int C = HD >= 128 ? 8 : HD / 16;  // channels of a word
   union { h8 v; h2 p[4]; } r[C];
 #pragma unroll
@@ -242,8 +344,8 @@ __device__ __forceinline__ void value_frags(const Tile<HD> &x, int lane, const _
     const unsigned odd = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
 #pragma unroll
     for (int c = 0; c < C; c += 2) {
-      r[c].p[e] = codes2(even, c >> 1) * sc.s[e];
-      r[c + 1].p[e] = codes2(odd, c >> 1) * sc.s[e];
+      r[c].p[e] = codes2(even, c >> 1) * sc[e];
+      r[c + 1].p[e] = codes2(odd, c >> 1) * sc[e];
     }
   }
 #pragma unroll
@@ -256,52 +358,35 @@ __device__ __forceinline__ void store_out(void *out, int64_t e, float a, float b
   else *reinterpret_cast<unsigned *>(static_cast<uint16_t *>(out) + e) = bf16x2_bits(a, b);
 }
 
-// Four waves take the 32-token tiles of a piece in turn, each for the same 16 NT query rows,
-// and join their sums at the end.
+// ---------------------------------------------------------------- query rows of a wave
+
+// The running maximum may lag by 2^lazy, and probabilities are held times 2^base, so at most
+// 2^15: what is smaller than 2^-32 of the largest (2^-38 for fp32 q) is lost under fp16's
+// smallest step.
+constexpr float lazy_of(bool f32) { return f32 ? 2.0f : 8.0f; }
+constexpr float base_of(bool f32) { return f32 ? 13.0f : 7.0f; }
+
+// 16 NT query rows: lane (i, quad) serves row 16 n + i of each tile n.
+template <int HD, int NT, bool F32>
+struct Rows {
+  h8 q[NT][F32 ? 2 : 1][HD / 32];  // fp16 halves: channels quad HD/4 + 8 s ..
+  float c[NT];                     // score times c = log2 of the unnormalised probability
+  float m[NT], l[NT];              // running maximum (log2), this lane's share of the sum
+  int lim[NT];                     // the first token that the row does not see
+  f4 acc[NT][HD / 16];             // channel (4 quad + r) HD/16 + d of row i in acc[n][d][r]
+};
+
 template <int HD, int NT, bool F32, bool EXACT>
-__global__ void __launch_bounds__(256) k_kv_attn_rows(Attn p) {
-  constexpr int HALVES = F32 ? 2 : 1;        // fp16 halves of q and p
-  constexpr float kLazy = F32 ? 2.0f : 8.0f; // log2
-  // probabilities are held times 2^kBase, at most 2^15: what is smaller than 2^-32 of the
-  // largest (2^-38 for fp32 q) is lost under fp16's smallest step
-  constexpr float kBase = F32 ? 13.0f : 7.0f;
-  constexpr int DV = HD / 16, OROW = HD + 4;
-  __shared__ __align__(16) float smem[4 * 16 * OROW];
-  __shared__ _Float16 vs_lds[4][DV * kVsRow];
-  __shared__ float sm_m[4][16 * NT], sm_l[4][16 * NT];
-
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+__device__ __forceinline__ void load_rows(const Attn &p, const Job &j, int h, int r0, int rows,
+                                          int lane, Rows<HD, NT, F32> &x) {
   const int i = lane & 15, quad = lane >> 4;
-  int w = blockIdx.x;
-  const int piece = w % p.pieces;
-  w /= p.pieces;
-  const int rt = w % p.row_tiles;
-  w /= p.row_tiles;
-  const int h = w % p.kv_heads;
-  const Job j = job_of(p, w / p.kv_heads);
-  const int rows = j.nq * p.group, r0 = rt * (16 * NT);
-  if (r0 >= rows) return;
-  int t0 = piece * p.piece, t1 = min(j.len, t0 + p.piece);
-  if (t0 >= t1 && !p.direct) return;
-
-  // query rows: operands, score factors and the first token each may not see
-  h8 qf[NT][HALVES][HD / 32];
-  float c[NT], m[NT], l[NT];
-  int lim[NT];
-  f4 acc[NT][DV];
-  int lim_lo = j.len, lim_hi = j.len;
-  if (j.causal) {
-    lim_lo = min(j.len, max(0, j.len - j.nq + r0 / p.group + 1));
-    lim_hi = min(j.len, max(0, j.len - j.nq + (min(r0 + 16 * NT, rows) - 1) / p.group + 1));
-  }
-  t1 = min(t1, lim_hi);
   const float sc = p.scale * kLog2e * p.S_k[h];
   const float sign = sc < 0.0f ? -1.0f : 1.0f;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int r = min(r0 + 16 * n + i, rows - 1);
     const int tok = r / p.group, head = h * p.group + (r - tok * p.group);
-    lim[n] = j.causal ? min(j.len, j.len - j.nq + tok + 1) : j.len;
+    x.lim[n] = j.causal ? min(j.len, j.len - j.nq + tok + 1) : j.len;
     const int64_t at = (int64_t)(j.q0 + tok) * p.q_ts + head * p.q_hs + quad * (HD / 4);
     float v[HD / 4], amax = 0.0f;
 #pragma unroll
@@ -329,21 +414,103 @@ __global__ void __launch_bounds__(256) k_kv_attn_rows(Attn p) {
     amax = fmaxf(amax, xor32(amax));
     float inv;
     const float f = row_factor(amax, inv) * sign;
-    c[n] = fmaxf(fabsf(sc) * inv, 1e-37f);  // positive, so a hidden score stays -inf
-    m[n] = -INFINITY;
-    l[n] = 0.0f;
+    x.c[n] = fmaxf(fabsf(sc) * inv, 1e-37f);  // positive, so a hidden score stays -inf
+    x.m[n] = -INFINITY;
+    x.l[n] = 0.0f;
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float y = v[8 * s + e] * f;
         const _Float16 hi = (_Float16)y;
-        qf[n][0][s][e] = hi;
-        if (F32) qf[n][HALVES - 1][s][e] = (_Float16)(y - (float)hi);
+        x.q[n][0][s][e] = hi;
+        if (F32) x.q[n][F32 ? 1 : 0][s][e] = (_Float16)(y - (float)hi);
       }
 #pragma unroll
-    for (int d = 0; d < DV; ++d) acc[n][d] = (f4){0, 0, 0, 0};
+    for (int d = 0; d < HD / 16; ++d) x.acc[n][d] = (f4){0, 0, 0, 0};
   }
+}
+
+// Rows r0 .. r1 - 1 all see the tokens below lo, and none sees one from hi on.
+__device__ __forceinline__ void row_limits(const Attn &p, const Job &j, int r0, int r1, int &lo,
+                                           int &hi) {
+  lo = hi = j.len;
+  if (j.causal) {
+    lo = min(j.len, max(0, j.len - j.nq + r0 / p.group + 1));
+    hi = min(j.len, max(0, j.len - j.nq + (r1 - 1) / p.group + 1));
+  }
+}
+
+// Scores of hidden tokens of the tile at t: -inf.
+template <int NT>
+__device__ __forceinline__ void hide(f4 (*s)[2], const int *lim, int t, int t1, int ok, int quad) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int tt = t + 16 * u + 4 * quad + r;
+        if (tt >= lim[n] || tt >= t1 || !((ok >> u) & 1)) s[n][u][r] = -INFINITY;
+      }
+}
+
+// Scores of a 32-token tile to fp16 probabilities, as the second product's operand.
+template <int HD, int NT, bool F32>
+__device__ __forceinline__ void probabilities(f4 (*s)[2], Rows<HD, NT, F32> &x, h8 (*pf)[F32 ? 2 : 1]) {
+  constexpr float kLazy = lazy_of(F32), kBase = base_of(F32);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float mx = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
+                     fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3]))) * x.c[n];
+    if (__any(mx > x.m[n] + kLazy)) {
+      mx = fmaxf(mx, xor16(mx));
+      mx = fmaxf(mx, xor32(mx));
+      const float to = fmaxf(x.m[n], mx);
+      const float a = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(x.m[n] - to);
+      x.m[n] = to;
+      x.l[n] *= a;
+#pragma unroll
+      for (int d = 0; d < HD / 16; ++d) x.acc[n][d] *= a;
+    }
+    const float base = (x.m[n] == -INFINITY ? 0.0f : x.m[n]) - kBase;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][u][r], x.c[n], -base));
+        x.l[n] += e;
+        const _Float16 hi = (_Float16)e;
+        pf[n][0][4 * u + r] = hi;
+        if (F32) pf[n][F32 ? 1 : 0][4 * u + r] = (_Float16)(e - (float)hi);
+      }
+  }
+}
+
+// Four waves take the 32-token tiles of a piece in turn, each for the same 16 NT query rows,
+// and join their sums at the end.
+template <int HD, int NT, bool F32, bool EXACT>
+__global__ void __launch_bounds__(256) k_kv_attn_rows(Attn p) {
+  constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, OROW = HD + 4;
+  constexpr float kBase = base_of(F32);
+  __shared__ __align__(16) float smem[4 * 16 * OROW];
+  __shared__ __align__(16) _Float16 vs_lds[4][DV * kVsRow];
+  __shared__ float sm_m[4][16 * NT], sm_l[4][16 * NT];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int i = lane & 15, quad = lane >> 4;
+  Share sh;
+  if (!share_of(p, lane, sh)) return;
+  const Job j = sh.j;
+  const int h = sh.h, rows = j.nq * p.group, r0 = sh.rt * (16 * NT), t0 = sh.t0;
+  if (r0 >= rows) return;
+  int t1 = sh.t1;
+
+  Rows<HD, NT, F32> x;
+  load_rows<HD, NT, F32, EXACT>(p, j, h, r0, rows, lane, x);
+  int lim_lo, lim_hi;
+  row_limits(p, j, r0, min(r0 + 16 * NT, rows), lim_lo, lim_hi);
+  t1 = min(t1, lim_hi);
 
   Tile<HD> cur, nxt;
   int t = t0 + 32 * wave;
@@ -366,47 +533,12 @@ __global__ void __launch_bounds__(256) k_kv_attn_rows(Attn p) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int q = 0; q < HALVES; ++q)
-            s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[n][q][k], s[n][u], 0, 0, 0);
+            s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, x.q[n][q][k], s[n][u], 0, 0, 0);
       }
     }
-    if (t + 32 > lim_lo || cur.ok != 3) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int tt = t + 16 * u + 4 * quad + r;
-            if (tt >= lim[n] || tt >= t1 || !((cur.ok >> u) & 1)) s[n][u][r] = -INFINITY;
-          }
-    }
+    if (t + 32 > lim_lo || cur.ok != 3) hide<NT>(s, x.lim, t, t1, cur.ok, quad);
     h8 pf[NT][HALVES];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float mx = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
-                       fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3]))) * c[n];
-      if (__any(mx > m[n] + kLazy)) {
-        mx = fmaxf(mx, xor16(mx));
-        mx = fmaxf(mx, xor32(mx));
-        const float to = fmaxf(m[n], mx);
-        const float a = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[n] - to);
-        m[n] = to;
-        l[n] *= a;
-#pragma unroll
-        for (int d = 0; d < DV; ++d) acc[n][d] *= a;
-      }
-      const float base = (m[n] == -INFINITY ? 0.0f : m[n]) - kBase;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][u][r], c[n], -base));
-          l[n] += e;
-          const _Float16 hi = (_Float16)e;
-          pf[n][0][4 * u + r] = hi;
-          if (F32) pf[n][HALVES - 1][4 * u + r] = (_Float16)(e - (float)hi);
-        }
-    }
+    probabilities<HD, NT, F32>(s, x, pf);
 #pragma unroll
     for (int word = 0; word < (HD > 128 ? HD / 128 : 1); ++word) {
       constexpr int C = HD >= 128 ? 8 : HD / 16;
@@ -418,8 +550,8 @@ __global__ void __launch_bounds__(256) k_kv_attn_rows(Attn p) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int q = 0; q < HALVES; ++q)
-            acc[n][8 * word + d] =
-                __builtin_amdgcn_mfma_f32_16x16x32_f16(a[d], pf[n][q], acc[n][8 * word + d], 0, 0, 0);
+            x.acc[n][8 * word + d] =
+                __builtin_amdgcn_mfma_f32_16x16x32_f16(a[d], pf[n][q], x.acc[n][8 * word + d], 0, 0, 0);
     }
     cur = nxt;
   }
@@ -427,9 +559,9 @@ __global__ void __launch_bounds__(256) k_kv_attn_rows(Attn p) {
   // join the four waves
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    l[n] += xor16(l[n]);
-    l[n] += xor32(l[n]);
-    if (quad == 0) sm_m[wave][16 * n + i] = m[n], sm_l[wave][16 * n + i] = l[n];
+    x.l[n] += xor16(x.l[n]);
+    x.l[n] += xor32(x.l[n]);
+    if (quad == 0) sm_m[wave][16 * n + i] = x.m[n], sm_l[wave][16 * n + i] = x.l[n];
   }
   __syncthreads();
   const float S_v = p.S_v[h];
@@ -438,13 +570,13 @@ __global__ void __launch_bounds__(256) k_kv_attn_rows(Attn p) {
     float M = -INFINITY;
 #pragma unroll
     for (int k = 0; k < 4; ++k) M = fmaxf(M, sm_m[k][16 * n + i]);
-    const float a = m[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[n] - M);
+    const float a = x.m[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(x.m[n] - M);
     if (n) __syncthreads();
     float *o = smem + (wave * 16 + i) * OROW;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int d = 0; d < DV; ++d) o[DV * (4 * quad + r) + d] = acc[n][d][r] * a;
+      for (int d = 0; d < DV; ++d) o[DV * (4 * quad + r) + d] = x.acc[n][d][r] * a;
     __syncthreads();
     // sixteen lanes a row, pairs of channels
     const int row = threadIdx.x >> 4, r = r0 + 16 * n + row;
@@ -459,220 +591,394 @@ __global__ void __launch_bounds__(256) k_kv_attn_rows(Attn p) {
       }
       const int tok = r / p.group, head = h * p.group + (r - tok * p.group);
       const int64_t at = (int64_t)(j.q0 + tok) * p.heads + head;
-      const float f = p.direct ? (ll > 0.0f ? S_v / ll : 0.0f) : 1.0f;
+      const float f = sh.direct ? (ll > 0.0f ? S_v / ll : 0.0f) : 1.0f;
       for (int d = 2 * (threadIdx.x & 15); d < p.hd; d += 32) {
         float2 y = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 z = *reinterpret_cast<const float2 *>(smem + (k * 16 + row) * OROW + d);
-          y.x += z.x, y.y += z.y;
+          const f2 z = *reinterpret_cast<const f2 *>(smem + (k * 16 + row) * OROW + d);
+          y.x += z[0], y.y += z[1];
         }
-        if (p.direct)
+        if (sh.direct)
           store_out<F32>(p.out, at * p.hd + d, y.x * f, y.y * f);
         else
-          *reinterpret_cast<float2 *>(
-              p.opart + (((int64_t)(p.slot0 + piece) * p.tokens * p.heads + at) * p.hd + d)) = y;
+          *reinterpret_cast<float2 *>(p.opart + (sh.part + r) * p.hd + d) = y;
       }
       if ((threadIdx.x & 15) == 0) {
-        if (p.direct) {
+        if (sh.direct) {
           if (p.lse) p.lse[at] = ll > 0.0f ? kLn2 * (mm - kBase + __builtin_amdgcn_logf(ll)) : -INFINITY;
         } else {
-          p.ml[(int64_t)(p.slot0 + piece) * p.tokens * p.heads + at] = make_float2(mm - kBase, ll);
+          p.ml[sh.part + r] = make_float2(mm - kBase, ll);
         }
       }
     }
   }
 }
 
-// Join the partial sums of a row: one wave per (token, head). Slots 0 .. n_prefix - 1 are the
-// prefix's pieces, then those of the sequence's own tokens.
+// Many query rows over one token list (a shared prefix, a prompt): the four waves of a
+// workgroup hold 16 NT rows each. A stage is 128 tokens: every wave dequantises one 32-token
+// tile into LDS, as ready MFMA operands in lane order (16 bytes a lane, no bank conflicts), and
+// all waves read all four tiles.
+template <int HD, int NT, bool F32, bool EXACT, int PER_SIMD>
+__global__ void __launch_bounds__(256, PER_SIMD) k_kv_attn_tile(Attn p) {
+  constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, KS = HD / 32;
+  constexpr float kBase = base_of(F32);
+  __shared__ h8 kfrag[4][2 * KS][64], vfrag[4][DV][64];
+  __shared__ __align__(16) _Float16 vs_lds[4][DV * kVsRow];
+  __shared__ int oks[4];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int i = lane & 15, quad = lane >> 4;
+  Share sh;
+  if (!share_of(p, lane, sh)) return;
+  const Job j = sh.j;
+  const int h = sh.h, rows = j.nq * p.group, R0 = sh.rt * (64 * NT), t0 = sh.t0;
+  if (R0 >= rows) return;
+  int t1 = sh.t1;
+  const int r0 = R0 + wave * 16 * NT;
+
+  Rows<HD, NT, F32> x;
+  load_rows<HD, NT, F32, EXACT>(p, j, h, r0, rows, lane, x);
+  int lim_lo, lim_hi, none;
+  row_limits(p, j, R0, min(R0 + 64 * NT, rows), none, lim_hi);
+  t1 = min(t1, lim_hi);
+  row_limits(p, j, min(r0, rows - 1), min(r0 + 16 * NT, rows), lim_lo, lim_hi);
+  if (r0 >= rows) lim_hi = 0;  // a wave without rows only dequantises
+
+  Tile<HD> cur, nxt;
+  if (t0 < t1) load_tile<HD, EXACT>(p, j, h, t0 + 32 * wave, t1, lane, cur);
+  for (int t = t0; t < t1; t += 128) {
+    if (t + 128 < t1) load_tile<HD, EXACT>(p, j, h, t + 128 + 32 * wave, t1, lane, nxt);
+    stage_value_scales<HD>(cur, lane, vs_lds[wave]);
+    if (t > t0) __syncthreads();  // the last stage has been read
+    if (lane == 0) oks[wave] = cur.ok;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      h2 ksc[HD / 128 > 0 ? HD / 128 : 1];
+#pragma unroll
+      for (int k = 0; k < (HD / 128 > 0 ? HD / 128 : 1); ++k) ksc[k] = scales2(cur.ks[u], k);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) kfrag[wave][u * KS + k][lane] = key_step<HD>(cur, u, k, ksc);
+    }
+#pragma unroll
+    for (int word = 0; word < (HD > 128 ? HD / 128 : 1); ++word) {
+      constexpr int C = HD >= 128 ? 8 : HD / 16;
+      h8 a[C];
+      value_frags<HD>(cur, lane, vs_lds[wave], word, a);
+#pragma unroll
+      for (int d = 0; d < C; ++d) vfrag[wave][8 * word + d][lane] = a[d];
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k4 = 0; k4 < 4; ++k4) {
+      const int tt = t + 32 * k4;
+      if (tt >= t1 || tt >= lim_hi) break;
+      f4 s[NT][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][u] = (f4){0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const h8 a = kfrag[k4][u * KS + k][lane];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int q = 0; q < HALVES; ++q)
+              s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, x.q[n][q][k], s[n][u], 0, 0, 0);
+        }
+      }
+      const int ok = __builtin_amdgcn_readfirstlane(oks[k4]);
+      if (tt + 32 > lim_lo || ok != 3) hide<NT>(s, x.lim, tt, t1, ok, quad);
+      h8 pf[NT][HALVES];
+      probabilities<HD, NT, F32>(s, x, pf);
+#pragma unroll
+      for (int d = 0; d < DV; ++d) {
+        const h8 a = vfrag[k4][d][lane];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int q = 0; q < HALVES; ++q)
+            x.acc[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf[n][q], x.acc[n][d], 0, 0, 0);
+      }
+    }
+    cur = nxt;
+  }
+
+  // each lane holds HD/16 consecutive channels of its row four times
+  const float S_v = p.S_v[h];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float l = x.l[n];
+    l += xor16(l);
+    l += xor32(l);
+    const int r = r0 + 16 * n + i;
+    if (r >= rows) continue;
+    const int tok = r / p.group, head = h * p.group + (r - tok * p.group);
+    const int64_t at = (int64_t)(j.q0 + tok) * p.heads + head;
+    const float f = sh.direct ? (l > 0.0f ? S_v / l : 0.0f) : 1.0f;
+#pragma unroll
+    for (int r4 = 0; r4 < 4; ++r4) {
+      const int ch = DV * (4 * quad + r4);
+      if (EXACT || ch < p.hd) {
+#pragma unroll
+        for (int d = 0; d < DV; d += 2) {
+          const float a = x.acc[n][d][r4] * f, b = x.acc[n][d + 1][r4] * f;
+          if (sh.direct)
+            store_out<F32>(p.out, at * p.hd + ch + d, a, b);
+          else
+            *reinterpret_cast<float2 *>(p.opart + (sh.part + r) * p.hd + ch + d) = make_float2(a, b);
+        }
+      }
+    }
+    if (quad == 0) {
+      if (sh.direct) {
+        if (p.lse) p.lse[at] = l > 0.0f ? kLn2 * (x.m[n] - kBase + __builtin_amdgcn_logf(l)) : -INFINITY;
+      } else {
+        p.ml[sh.part + r] = make_float2(x.m[n] - kBase, l);
+      }
+    }
+  }
+}
+
+// Join the partial sums of a row, one workgroup per (token, head): HD / 4 lanes take four
+// channels each, and the 1024 / HD groups of lanes take the row's pieces in turn. The
+// prefix's pieces come first, then those of the sequence's own tokens.
 struct Join {
-  const float *opart, *S_v;
-  const float2 *ml;
+  const float *opart, *opart_own, *S_v;
+  const float2 *ml, *ml_own;
   void *out;
   float *lse;
   const int32_t *q_offsets, *kv_lens;
-  int tokens, heads, group, hd, max_q, max_len, n_prefix, piece;
+  int tokens, heads, kv_heads, group, hd, max_q, max_len, batch, n_prefix;
+  float target;
 };
 
-template <bool F32>
+template <int HD, bool F32>
 __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
+  constexpr int LANES = HD / 4, GROUPS = 256 / LANES;
+  __shared__ f4 so[GROUPS][LANES];
+  __shared__ float sm_m[GROUPS], sm_l[GROUPS];
   const int lane = threadIdx.x & 63, b = blockIdx.y;
-  const int idx = blockIdx.x * 4 + ((int)threadIdx.x >> 6);
-  const int i = idx / p.heads, head = idx - i * p.heads;
+  const int g = threadIdx.x / LANES, c = threadIdx.x % LANES;
+  const int i = blockIdx.x / p.heads, head = blockIdx.x - i * p.heads;
   int lo = b * p.max_q, hi = lo + p.max_q;
   if (p.q_offsets) {
     lo = min(max(p.q_offsets[b], 0), p.tokens);
     hi = min(max(p.q_offsets[b + 1], lo), min(p.tokens, lo + p.max_q));
   }
   if (lo + i >= hi) return;
-  int n = p.n_prefix;
-  if (p.kv_lens) {
-    const int len = min(max(p.kv_lens[b], 0), p.max_len);
-    n += (len + p.piece - 1) / p.piece;
+  int own0 = b, n = p.n_prefix;
+  if (p.target > 0.0f) {
+    const Piece x = find_piece(p.kv_lens, p.batch, p.max_len, p.target, 0, b, lane);
+    own0 = x.first, n += x.count;
+  } else if (p.kv_lens) {
+    n += 1;
   }
-  const int64_t rows = (int64_t)p.tokens * p.heads, at = (int64_t)(lo + i) * p.heads + head;
+  const int h = head / p.group, gr = head - h * p.group;
+  const int64_t rows = (int64_t)p.tokens * p.group, own_rows = (int64_t)p.max_q * p.group;
+  const int64_t at = h * rows + (int64_t)(lo + i) * p.group + gr;      // in a prefix slot
+  const int64_t own_at = ((int64_t)own0 * p.kv_heads + h) * own_rows + (int64_t)i * p.group + gr;
+  const int64_t step = rows * p.kv_heads, own_step = own_rows * p.kv_heads;
   float M = -INFINITY, L = 0.0f;
-  for (int k = lane; k < n; k += 64) M = fmaxf(M, p.ml[k * rows + at].x);
-#pragma unroll
-  for (int off = 32; off; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
-  const float S = p.S_v[head / p.group];
-  float2 y[2] = {};  // head_dim <= 256
-  const int d = 2 * lane;
-  for (int k0 = 0; k0 < n; k0 += 64) {
-    float2 mine = make_float2(-INFINITY, 0.0f);
-    if (k0 + lane < n) mine = p.ml[(k0 + lane) * rows + at];
-    const float wgt = mine.y > 0.0f ? __builtin_amdgcn_exp2f(mine.x - M) : 0.0f;
-    float part = mine.y * wgt;
-#pragma unroll
-    for (int off = 32; off; off >>= 1) part += __shfl_xor(part, off, 64);
-    L += part;
-    const int end = min(64, n - k0);
-    for (int k = 0; k < end; ++k) {
-      const float a = __shfl(wgt, k, 64);
-      if (a == 0.0f) continue;  // the same for the wave: the piece may be unwritten
-      const float *o = p.opart + ((k0 + k) * rows + at) * p.hd;
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (d + 128 * s < p.hd) {
-          const float2 z = *reinterpret_cast<const float2 *>(o + d + 128 * s);
-          y[s].x = __builtin_fmaf(a, z.x, y[s].x), y[s].y = __builtin_fmaf(a, z.y, y[s].y);
-        }
+  f4 y = {0, 0, 0, 0};
+  const bool in = 4 * c < p.hd;
+#pragma unroll 4
+  for (int k = g; k < n; k += GROUPS) {
+    const bool pre = k < p.n_prefix;
+    const int64_t row = pre ? at + k * step : own_at + (k - p.n_prefix) * own_step;
+    const float2 ml = (pre ? p.ml : p.ml_own)[row];
+    f4 o = {0, 0, 0, 0};
+    if (in) o = *reinterpret_cast<const f4 *>((pre ? p.opart : p.opart_own) + row * p.hd + 4 * c);
+    if (ml.y > 0.0f) {  // else the piece holds nothing the row sees
+      const float to = fmaxf(M, ml.x);
+      const float a = __builtin_amdgcn_exp2f(M - to), e = __builtin_amdgcn_exp2f(ml.x - to);
+      M = to;
+      L = L * a + ml.y * e;
+      y = y * a + o * e;
     }
   }
-  const float f = L > 0.0f ? S / L : 0.0f;
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-    if (d + 128 * s < p.hd) store_out<F32>(p.out, at * p.hd + d + 128 * s, y[s].x * f, y[s].y * f);
-  if (lane == 0 && p.lse) p.lse[at] = L > 0.0f ? kLn2 * (M + __builtin_amdgcn_logf(L)) : -INFINITY;
+  if (c == 0) sm_m[g] = M, sm_l[g] = L;
+  so[g][c] = y;
+  __syncthreads();
+  if (g) return;
+  M = sm_m[0];
+  for (int k = 1; k < GROUPS; ++k) M = fmaxf(M, sm_m[k]);
+  L = 0.0f;
+  y = (f4){0, 0, 0, 0};
+  for (int k = 0; k < GROUPS; ++k) {
+    if (!(sm_l[k] > 0.0f)) continue;
+    const float e = __builtin_amdgcn_exp2f(sm_m[k] - M);
+    L += sm_l[k] * e;
+    y += so[k][c] * e;
+  }
+  const int64_t to = (int64_t)(lo + i) * p.heads + head;
+  const float f = L > 0.0f ? p.S_v[h] / L : 0.0f;
+  if (in) {
+    store_out<F32>(p.out, to * p.hd + 4 * c, y[0] * f, y[1] * f);
+    store_out<F32>(p.out, to * p.hd + 4 * c + 2, y[2] * f, y[3] * f);
+  }
+  if (c == 0 && p.lse) p.lse[to] = L > 0.0f ? kLn2 * (M + __builtin_amdgcn_logf(L)) : -INFINITY;
 }
 
 // ---------------------------------------------------------------- plan and launch
 
 namespace {
 
-struct Part {  // one launch: the prefix or the sequences' own tokens
-  int nt, row_tiles, piece, pieces;
+struct Part {    // one launch: the prefix or the sequences' own tokens
+  int nt, tile;  // 16-row tiles of a wave; tile: k_kv_attn_tile instead of k_kv_attn_rows
+  int row_tiles, slots, piece;
+  float target;
 };
 
 struct Plan {
   Part prefix, own;
-  int max_len;
+  int direct;
 };
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Pieces so that about `want` workgroups run, each at least 128 tokens (a tile for each wave).
-Part plan_part(const KvAttention &a, int64_t rows, int64_t jobs, int64_t len) {
-  Part r;
-  const int top = a.cache->head_dim > 128 ? 2 : (a.dtype == NVFP4_DTYPE_F32 ? 2 : 4);
-  r.nt = rows <= 16 ? 1 : (rows <= 32 || top == 2 ? 2 : 4);
-  r.row_tiles = (int)cdiv(rows, 16 * r.nt);
-  const int64_t units = jobs * a.cache->kv_heads * r.row_tiles;
-  const int64_t want = 2048;
-  int64_t pieces = cdiv(want, units);
-  int64_t piece = cdiv(cdiv(len, pieces), 128) * 128;
-  if (piece < 128) piece = 128;
-  r.piece = (int)piece;
-  r.pieces = (int)(len > 0 ? cdiv(len, piece) : 1);
+Part plan_rows(const KvAttention &a, int64_t rows) {
+  Part r = {};
+  const bool wide = a.cache->head_dim > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
+  r.tile = rows > 64;
+  if (r.tile) r.nt = wide || f32 ? 1 : TILE_NT;
+  else r.nt = rows <= 16 ? 1 : (rows <= 32 || wide || f32 ? 2 : 4);
+  r.row_tiles = (int)cdiv(rows, (r.tile ? 64 : 16) * r.nt);
   return r;
 }
 
 Plan plan_of(const KvAttention &a) {
-  Plan p;
+  Plan p = {};
   const int64_t G = a.heads / a.cache->kv_heads;
-  p.max_len = (int)a.max_kv;
-  p.prefix = Part{0, 0, 0, 0};
-  p.own = Part{0, 0, 0, 0};
-  if (a.prefix_len > 0) p.prefix = plan_part(a, a.tokens * G, 1, a.prefix_len);
-  if (a.max_kv > 0 || a.prefix_len == 0) p.own = plan_part(a, a.max_q * G, a.batch, a.max_kv);
+  if (a.prefix_len > 0) {
+    Part &r = p.prefix = plan_rows(a, a.tokens * G);
+    const int64_t units = a.cache->kv_heads * r.row_tiles, want = r.tile ? WANT_TILE : WANT_ROWS;
+    r.piece = (int)(cdiv(a.prefix_len, 128 * cdiv(want, units)) * 128);
+    r.slots = (int)cdiv(a.prefix_len, r.piece);
+  }
+  if (a.max_kv > 0 || a.prefix_len == 0) {
+    Part &r = p.own = plan_rows(a, a.max_q * G);
+    const int64_t units = a.cache->kv_heads * r.row_tiles, want = r.tile ? WANT_TILE : WANT_ROWS;
+    const int64_t most = a.batch * cdiv(a.max_kv, 128);  // pieces of 128 tokens
+    r.slots = (int)a.batch;
+    if (a.max_kv > 128 && units < want) {
+      r.target = (float)want / (float)units;
+      const int64_t n = want / units + 1 + a.batch;
+      r.slots = (int)(n < most ? n : most);
+    }
+  }
+  p.direct = p.prefix.slots == 0 ? p.own.target == 0.0f : p.prefix.slots == 1 && p.own.slots == 0;
   return p;
 }
 
 template <int HD, bool F32, bool EXACT>
-void launch_rows(const Attn &p, int nt, unsigned grid, hipStream_t st) {
+void launch_rows(const Attn &p, const Part &r, unsigned grid, hipStream_t st) {
   const dim3 g(grid), b(256);
-  if (nt == 1) hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT>), g, b, 0, st, p);
-  else if (nt == 2) hipLaunchKernelGGL((k_kv_attn_rows<HD, 2, F32, EXACT>), g, b, 0, st, p);
-  else if constexpr (HD <= 128 && !F32)
+  if (r.tile) {
+    if constexpr (HD <= 128 && !F32)
+      hipLaunchKernelGGL((k_kv_attn_tile<HD, TILE_NT, F32, EXACT, TILE_OCC>), g, b, 0, st, p);
+    else
+      hipLaunchKernelGGL((k_kv_attn_tile<HD, 1, F32, EXACT, 1>), g, b, 0, st, p);
+  } else if (r.nt == 1) {
+    hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT>), g, b, 0, st, p);
+  } else if (r.nt == 2) {
+    hipLaunchKernelGGL((k_kv_attn_rows<HD, 2, F32, EXACT>), g, b, 0, st, p);
+  } else if constexpr (HD <= 128 && !F32) {
     hipLaunchKernelGGL((k_kv_attn_rows<HD, 4, F32, EXACT>), g, b, 0, st, p);
+  }
 }
 
 template <int HD, bool F32>
-void launch_exact(const Attn &p, int nt, unsigned grid, hipStream_t st) {
-  if (p.hd == HD) launch_rows<HD, F32, true>(p, nt, grid, st);
-  else launch_rows<HD, F32, false>(p, nt, grid, st);
+void launch_exact(const Attn &p, const Part &r, unsigned grid, hipStream_t st) {
+  if (p.hd == HD) launch_rows<HD, F32, true>(p, r, grid, st);
+  else launch_rows<HD, F32, false>(p, r, grid, st);
 }
 
 template <bool F32>
-void launch_hd(const Attn &p, int nt, unsigned grid, hipStream_t st) {
-  if (p.hd <= 64) launch_exact<64, F32>(p, nt, grid, st);
-  else if (p.hd <= 128) launch_exact<128, F32>(p, nt, grid, st);
-  else launch_exact<256, F32>(p, nt, grid, st);
+void launch_hd(const Attn &p, const Part &r, unsigned grid, hipStream_t st) {
+  if (p.hd <= 64) launch_exact<64, F32>(p, r, grid, st);
+  else if (p.hd <= 128) launch_exact<128, F32>(p, r, grid, st);
+  else launch_exact<256, F32>(p, r, grid, st);
 }
 
-int64_t part_grid(const KvAttention &a, const Part &r, int64_t jobs) {
-  return jobs * a.cache->kv_heads * r.row_tiles * r.pieces;
+int64_t part_grid(const KvAttention &a, const Part &r) {
+  return (int64_t)r.slots * a.cache->kv_heads * r.row_tiles;
+}
+
+// partial rows of the two launches
+int64_t prefix_rows(const KvAttention &a, const Plan &p) {
+  return (int64_t)p.prefix.slots * a.tokens * a.heads;
+}
+int64_t own_rows(const KvAttention &a, const Plan &p) {
+  return (int64_t)p.own.slots * a.max_q * a.heads;
+}
+
+template <int HD>
+void launch_join(const Join &p, bool f32, dim3 g, hipStream_t st) {
+  if (f32) hipLaunchKernelGGL((k_kv_attn_join<HD, true>), g, dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((k_kv_attn_join<HD, false>), g, dim3(256), 0, st, p);
 }
 
 }  // namespace
 
 bool kv_attention_fits(const KvAttention &a) {
   const Plan p = plan_of(a);
-  return part_grid(a, p.prefix, 1) <= INT32_MAX && part_grid(a, p.own, a.batch) <= INT32_MAX;
+  return part_grid(a, p.prefix) <= INT32_MAX && part_grid(a, p.own) <= INT32_MAX;
 }
 
 size_t kv_attention_workspace_size(const KvAttention &a) {
   const Plan p = plan_of(a);
-  const int64_t slots = p.prefix.pieces + p.own.pieces;
-  if (slots <= 1) return 0;
-  return (size_t)(slots * a.tokens * a.heads * (a.cache->head_dim * 4 + 8));
+  if (p.direct) return 0;
+  return (size_t)((prefix_rows(a, p) + own_rows(a, p)) * (a.cache->head_dim * 4 + 8));
 }
 
 int launch_kv_attention(const KvAttention &a, hipStream_t st) {
   const Plan plan = plan_of(a);
   const nvfp4_kv_cache &c = *a.cache;
-  const int slots = plan.prefix.pieces + plan.own.pieces;
-  const int64_t rows = a.tokens * a.heads;
+  const int64_t n_pre = prefix_rows(a, plan), n_own = own_rows(a, plan);
   Attn p = {};
   p.kc = c.k_codes, p.ks = c.k_scales, p.vc = c.v_codes, p.vs = c.v_scales;
   p.S_k = c.S_k, p.S_v = c.S_v;
   p.q = a.q, p.q_ts = a.q_ts, p.q_hs = a.q_hs, p.q_offsets = a.q_offsets, p.kv_lens = a.kv_lens;
   p.tokens = (int)a.tokens, p.heads = (int)a.heads, p.kv_heads = (int)c.kv_heads;
-  p.group = (int)(a.heads / c.kv_heads), p.hd = (int)c.head_dim;
+  p.group = (int)(a.heads / c.kv_heads), p.hd = (int)c.head_dim, p.batch = (int)a.batch;
   p.page_shift = __builtin_ctzll((unsigned long long)c.page_size);
-  p.pages = (int)c.pages, p.max_q = (int)a.max_q, p.scale = a.scale;
-  p.direct = slots <= 1;
+  p.pages = (int)c.pages, p.max_q = (int)a.max_q, p.scale = a.scale, p.direct = plan.direct;
   p.out = a.out, p.lse = a.lse;
-  p.opart = static_cast<float *>(a.workspace);
-  p.ml = reinterpret_cast<float2 *>(p.opart + (size_t)slots * rows * c.head_dim);
+  float *opart = static_cast<float *>(a.workspace), *own = opart + n_pre * c.head_dim;
+  float2 *ml = reinterpret_cast<float2 *>(own + n_own * c.head_dim), *ml_own = ml + n_pre;
   const bool f32 = a.dtype == NVFP4_DTYPE_F32;
-  if (plan.prefix.pieces) {
+  if (plan.prefix.slots) {
     Attn x = p;
     x.prefix = 1, x.table = a.prefix_pages, x.max_len = (int)a.prefix_len;
-    x.piece = plan.prefix.piece, x.pieces = plan.prefix.pieces, x.row_tiles = plan.prefix.row_tiles;
-    const unsigned g = (unsigned)part_grid(a, plan.prefix, 1);
-    if (f32) launch_hd<true>(x, plan.prefix.nt, g, st);
-    else launch_hd<false>(x, plan.prefix.nt, g, st);
+    x.piece = plan.prefix.piece, x.slots = plan.prefix.slots, x.row_tiles = plan.prefix.row_tiles;
+    x.opart = opart, x.ml = ml;
+    const unsigned g = (unsigned)part_grid(a, plan.prefix);
+    if (f32) launch_hd<true>(x, plan.prefix, g, st);
+    else launch_hd<false>(x, plan.prefix, g, st);
   }
-  if (plan.own.pieces) {
+  if (plan.own.slots) {
     Attn x = p;
-    x.table = a.block_table, x.table_width = a.table_width, x.max_len = plan.max_len;
-    x.causal = a.causal, x.slot0 = plan.prefix.pieces;
-    x.piece = plan.own.piece, x.pieces = plan.own.pieces, x.row_tiles = plan.own.row_tiles;
-    const unsigned g = (unsigned)part_grid(a, plan.own, a.batch);
-    if (f32) launch_hd<true>(x, plan.own.nt, g, st);
-    else launch_hd<false>(x, plan.own.nt, g, st);
+    x.table = a.block_table, x.table_width = a.table_width, x.max_len = (int)a.max_kv;
+    x.causal = a.causal, x.target = plan.own.target;
+    x.slots = plan.own.slots, x.row_tiles = plan.own.row_tiles;
+    x.opart = own, x.ml = ml_own;
+    const unsigned g = (unsigned)part_grid(a, plan.own);
+    if (f32) launch_hd<true>(x, plan.own, g, st);
+    else launch_hd<false>(x, plan.own, g, st);
   }
-  if (slots > 1) {
+  if (!plan.direct) {
     Join x = {};
-    x.opart = p.opart, x.ml = p.ml, x.S_v = c.S_v, x.out = a.out, x.lse = a.lse;
-    x.q_offsets = a.q_offsets, x.kv_lens = a.kv_lens;
-    x.tokens = p.tokens, x.heads = p.heads, x.group = p.group, x.hd = p.hd, x.max_q = p.max_q;
-    x.max_len = plan.max_len, x.n_prefix = plan.prefix.pieces, x.piece = plan.own.piece;
-    const dim3 g((unsigned)cdiv(a.max_q * a.heads, 4), (unsigned)a.batch);
-    if (f32) hipLaunchKernelGGL(k_kv_attn_join<true>, g, dim3(256), 0, st, x);
-    else hipLaunchKernelGGL(k_kv_attn_join<false>, g, dim3(256), 0, st, x);
+    x.opart = opart, x.opart_own = own, x.ml = ml, x.ml_own = ml_own;
+    x.S_v = c.S_v, x.out = a.out, x.lse = a.lse, x.q_offsets = a.q_offsets, x.kv_lens = a.kv_lens;
+    x.tokens = p.tokens, x.heads = p.heads, x.kv_heads = p.kv_heads, x.group = p.group, x.hd = p.hd;
+    x.max_q = p.max_q, x.max_len = (int)a.max_kv, x.batch = p.batch;
+    x.n_prefix = plan.prefix.slots, x.target = plan.own.target;
+    const dim3 g((unsigned)(a.max_q * a.heads), (unsigned)a.batch);
+    if (p.hd <= 64) launch_join<64>(x, f32, g, st);
+    else if (p.hd <= 128) launch_join<128>(x, f32, g, st);
+    else launch_join<256>(x, f32, g, st);
   }
   return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
