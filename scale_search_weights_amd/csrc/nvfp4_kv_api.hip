@@ -101,12 +101,14 @@ int nvfp4_kv_write(const nvfp4_kv_cache *cache, const void *k, const void *v, in
   NVFP4_TRY(check_rows(k, dtype, tokens, cache->kv_heads, k_token_stride, k_head_stride));
   NVFP4_TRY(check_rows(v, dtype, tokens, cache->kv_heads, v_token_stride, v_head_stride));
   const hipStream_t st = as_stream(stream);
-  debug_check_finite_rows(k, dtype, tokens, cache->kv_heads, cache->head_dim, k_token_stride,
-                          k_head_stride, st);
-  debug_check_finite_rows(v, dtype, tokens, cache->kv_heads, cache->head_dim, v_token_stride,
-                          v_head_stride, st);
-  debug_check_scale(cache->S_k, cache->kv_heads, st);
-  debug_check_scale(cache->S_v, cache->kv_heads, st);
+  if (debug_checks_enabled()) {
+    debug_check_finite_rows(k, dtype, tokens, cache->kv_heads, cache->head_dim, k_token_stride,
+                            k_head_stride, st);
+    debug_check_finite_rows(v, dtype, tokens, cache->kv_heads, cache->head_dim, v_token_stride,
+                            v_head_stride, st);
+    debug_check_scale(cache->S_k, cache->kv_heads, st);
+    debug_check_scale(cache->S_v, cache->kv_heads, st);
+  }
   return launch_kv_write(*cache, k, v, dtype, tokens, k_token_stride, k_head_stride,
                          v_token_stride, v_head_stride, slots, st);
 }
@@ -120,7 +122,7 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, const int64_t *slots, int64_t n, 
   if (!slots || (!k && !v)) return NVFP4_ERR_NULL;
   if (!aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16)) return NVFP4_ERR_ALIGN;
   const hipStream_t st = as_stream(stream);
-  if (cache->pages > 0) {
+  if (cache->pages > 0 && debug_checks_enabled()) {
     debug_check_scale(cache->S_k, cache->kv_heads, st);
     debug_check_scale(cache->S_v, cache->kv_heads, st);
   }
@@ -163,10 +165,13 @@ int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const void *q, int dtype, in
   if (need && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
   if (need && !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
   const hipStream_t st = as_stream(stream);
-  debug_check_finite_rows(q, dtype, tokens, heads, cache->head_dim, q_token_stride, q_head_stride, st);
-  if (cache->pages > 0) {
-    debug_check_scale(cache->S_k, cache->kv_heads, st);
-    debug_check_scale(cache->S_v, cache->kv_heads, st);
+  if (debug_checks_enabled()) {
+    debug_check_finite_rows(q, dtype, tokens, heads, cache->head_dim, q_token_stride,
+                            q_head_stride, st);
+    if (cache->pages > 0) {
+      debug_check_scale(cache->S_k, cache->kv_heads, st);
+      debug_check_scale(cache->S_v, cache->kv_heads, st);
+    }
   }
   a.q = q, a.q_ts = q_token_stride, a.q_hs = q_head_stride, a.q_offsets = q_offsets;
   a.block_table = block_table, a.table_width = table_width;

@@ -14,9 +14,9 @@
 // of the cache: lane (i, quad) takes channels [quad HD/4, ..) of key token i, and channels
 // [i HD/16, ..) of the value tokens 4 quad + 0..3 and 16 + 4 quad + 0..3.
 //
-// Running maximum: it is raised (and the sums rescaled) only when a score exceeds it by more
-// than 2^kLazy; until then probabilities may exceed 1, which fp16 holds. A wave rescales a
-// few times per sequence instead of once per tile.
+// Running maximum: it is raised (and the sums rescaled) only when a probability relative to it
+// leaves fp16's range, a few times per sequence instead of once per tile, and no maximum is
+// taken in between: the sums show the overflow.
 #include "nvfp4_device.h"
 #include "nvfp4_kv.h"
 
@@ -31,6 +31,9 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.4426950408889634f;
 #ifndef WANT_ROWS
 #define WANT_ROWS 768
+#endif
+#ifndef ROWS_OCC
+#define ROWS_OCC 1
 #endif
 #ifndef WANT_TILE
 #define WANT_TILE 512
@@ -360,10 +363,9 @@ __device__ __forceinline__ void store_out(void *out, int64_t e, float a, float b
 
 // ---------------------------------------------------------------- query rows of a wave
 
-// The running maximum may lag by 2^lazy, and probabilities are held times 2^base, so at most
-// 2^15: what is smaller than 2^-32 of the largest (2^-38 for fp32 q) is lost under fp16's
-// smallest step.
-constexpr float lazy_of(bool f32) { return f32 ? 2.0f : 8.0f; }
+// Probabilities are held times 2^base over the running maximum's, and the maximum is raised
+// when one passes 2^16, fp16's range. The row's largest is held at 2^base or more, so what is
+// smaller than 2^-32 of it (2^-38 for fp32 q) is lost under fp16's smallest step.
 constexpr float base_of(bool f32) { return f32 ? 13.0f : 7.0f; }
 
 // 16 NT query rows: lane (i, quad) serves row 16 n + i of each tile n.
@@ -371,7 +373,8 @@ template <int HD, int NT, bool F32>
 struct Rows {
   h8 q[NT][F32 ? 2 : 1][HD / 32];  // fp16 halves: channels quad HD/4 + 8 s ..
   float c[NT];                     // score times c = log2 of the unnormalised probability
-  float m[NT], l[NT];              // running maximum (log2), this lane's share of the sum
+  float off[NT];                   // base - running maximum (log2); +inf before the first token
+  float l[NT];                     // this lane's share of the sum of the probabilities
   int lim[NT];                     // the first token that the row does not see
   f4 acc[NT][HD / 16];             // channel (4 quad + r) HD/16 + d of row i in acc[n][d][r]
 };
@@ -415,7 +418,7 @@ __device__ __forceinline__ void load_rows(const Attn &p, const Job &j, int h, in
     float inv;
     const float f = row_factor(amax, inv) * sign;
     x.c[n] = fmaxf(fabsf(sc) * inv, 1e-37f);  // positive, so a hidden score stays -inf
-    x.m[n] = -INFINITY;
+    x.off[n] = INFINITY;
     x.l[n] = 0.0f;
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s)
@@ -455,42 +458,64 @@ __device__ __forceinline__ void hide(f4 (*s)[2], const int *lim, int t, int t1, 
       }
 }
 
-// Scores of a 32-token tile to fp16 probabilities, as the second product's operand.
+// exp2(score c + off) as fp16 (two halves for fp32 q), the second product's operand; returns
+// the sum of the lane's eight before that rounding.
+template <bool F32>
+__device__ __forceinline__ float exponentials(const f4 *s, float c, float off, h8 *pf) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][r], c, off));
+      sum += e;
+      const _Float16 hi = (_Float16)e;
+      pf[0][4 * u + r] = hi;
+      if (F32) pf[F32 ? 1 : 0][4 * u + r] = (_Float16)(e - (float)hi);
+    }
+  return sum;
+}
+
+// Scores of a 32-token tile to probabilities, held times 2^base over the running maximum's. No
+// maximum is taken while a lane's eight sum to less than fp16's range (before the first
+// visible token the offset is +inf, and the sum infinite or NaN); only then is the maximum
+// raised and everything so far rescaled.
 template <int HD, int NT, bool F32>
 __device__ __forceinline__ void probabilities(f4 (*s)[2], Rows<HD, NT, F32> &x, h8 (*pf)[F32 ? 2 : 1]) {
-  constexpr float kLazy = lazy_of(F32), kBase = base_of(F32);
+  constexpr float kBase = base_of(F32);
+  float sum[NT];
+  bool fits = true;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    float mx = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
-                     fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3]))) * x.c[n];
-    if (__any(mx > x.m[n] + kLazy)) {
+    sum[n] = exponentials<F32>(s[n], x.c[n], x.off[n], pf[n]);
+    fits = fits && sum[n] < 65504.0f;
+  }
+  if (!__all(fits)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float mx = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
+                       fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3]))) * x.c[n];
       mx = fmaxf(mx, xor16(mx));
       mx = fmaxf(mx, xor32(mx));
-      const float to = fmaxf(x.m[n], mx);
-      const float a = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(x.m[n] - to);
-      x.m[n] = to;
+      const float m = kBase - x.off[n];  // -inf before the first visible token
+      const float to = fmaxf(m, mx);
+      const bool none = to == -INFINITY;
+      const float a = none ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+      x.off[n] = kBase - to;
       x.l[n] *= a;
 #pragma unroll
       for (int d = 0; d < HD / 16; ++d) x.acc[n][d] *= a;
+      sum[n] = exponentials<F32>(s[n], x.c[n], none ? 0.0f : x.off[n], pf[n]);
     }
-    const float base = (x.m[n] == -INFINITY ? 0.0f : x.m[n]) - kBase;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][u][r], x.c[n], -base));
-        x.l[n] += e;
-        const _Float16 hi = (_Float16)e;
-        pf[n][0][4 * u + r] = hi;
-        if (F32) pf[n][F32 ? 1 : 0][4 * u + r] = (_Float16)(e - (float)hi);
-      }
   }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) x.l[n] += sum[n];
 }
 
 // Four waves take the 32-token tiles of a piece in turn, each for the same 16 NT query rows,
 // and join their sums at the end.
 template <int HD, int NT, bool F32, bool EXACT>
-__global__ void __launch_bounds__(256) k_kv_attn_rows(Attn p) {
+__global__ void __launch_bounds__(256, ROWS_OCC) k_kv_attn_rows(Attn p) {
   constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, OROW = HD + 4;
   constexpr float kBase = base_of(F32);
   __shared__ __align__(16) float smem[4 * 16 * OROW];
@@ -561,7 +586,7 @@ __global__ void __launch_bounds__(256) k_kv_attn_rows(Attn p) {
   for (int n = 0; n < NT; ++n) {
     x.l[n] += xor16(x.l[n]);
     x.l[n] += xor32(x.l[n]);
-    if (quad == 0) sm_m[wave][16 * n + i] = x.m[n], sm_l[wave][16 * n + i] = x.l[n];
+    if (quad == 0) sm_m[wave][16 * n + i] = kBase - x.off[n], sm_l[wave][16 * n + i] = x.l[n];
   }
   __syncthreads();
   const float S_v = p.S_v[h];
@@ -570,7 +595,8 @@ __global__ void __launch_bounds__(256) k_kv_attn_rows(Attn p) {
     float M = -INFINITY;
 #pragma unroll
     for (int k = 0; k < 4; ++k) M = fmaxf(M, sm_m[k][16 * n + i]);
-    const float a = x.m[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(x.m[n] - M);
+    const float m = kBase - x.off[n];
+    const float a = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
     if (n) __syncthreads();
     float *o = smem + (wave * 16 + i) * OROW;
 #pragma unroll
@@ -733,9 +759,9 @@ __global__ void __launch_bounds__(256, PER_SIMD) k_kv_attn_tile(Attn p) {
     }
     if (quad == 0) {
       if (sh.direct) {
-        if (p.lse) p.lse[at] = l > 0.0f ? kLn2 * (x.m[n] - kBase + __builtin_amdgcn_logf(l)) : -INFINITY;
+        if (p.lse) p.lse[at] = l > 0.0f ? kLn2 * (__builtin_amdgcn_logf(l) - x.off[n]) : -INFINITY;
       } else {
-        p.ml[sh.part + r] = make_float2(x.m[n] - kBase, l);
+        p.ml[sh.part + r] = make_float2(-x.off[n], l);
       }
     }
   }

@@ -79,6 +79,7 @@ class KVCache:
         self.S_k, self.S_v = S_k, S_v
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, size, 2 * half
         self.device = k_codes.device
+        self._index = self.device.index
         self._c = _Cache(*(t.data_ptr() for t in (k_codes, k_scales, v_codes, v_scales, S_k, S_v)),
                          pages, size, heads, 2 * half)
         self._ref = ctypes.addressof(self._c)
@@ -93,6 +94,10 @@ class KVCache:
                    S_k, S_v)
 
 
+_BF16, _F32, _I32, _INT64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream without a Stream object
+
+
 def _rows(t, name: str, cache: KVCache, heads: int | None):
     """A strided [tokens, heads, head_dim] tensor whose rows the kernels read in 16-byte
     pieces; returns its dtype code and its token and head strides."""
@@ -101,31 +106,28 @@ def _rows(t, name: str, cache: KVCache, heads: int | None):
     if t.device != cache.device:
         raise ValueError(f"{name} is on {t.device}, expected {cache.device}")
     dt = _dt(t)
-    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {cache.head_dim}], got {list(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {cache.head_dim}], got {list(shape)}")
     ts, hs, ds = t.stride()
-    if t.shape[0] <= 1:  # the stride of a single token or head says nothing
+    if shape[0] <= 1:  # the stride of a single token or head says nothing
         ts = 0
-    if t.shape[1] <= 1:
+    if shape[1] <= 1:
         hs = 0
-    unit = 8 if dt == nvfp4.DTYPE_BF16 else 4
-    if ds != 1 or ts % unit or hs % unit or t.data_ptr() % 16:
+    if ds != 1 or (ts | hs) & (7 if dt == nvfp4.DTYPE_BF16 else 3) or t.data_ptr() & 15:
         raise ValueError(f"{name} must be contiguous along head_dim, every row at a multiple of 16 bytes")
     return dt, ts, hs
 
 
-def _slots(slots, cache: KVCache, n: int | None = None):
-    _need(slots, "slots")
-    if slots.device != cache.device:
-        raise ValueError(f"slots is on {slots.device}, expected {cache.device}")
-    if slots.dtype != torch.int64 or slots.dim() != 1:
-        raise TypeError("slots must be int64 [tokens]")
-    if n is not None and slots.shape[0] != n:
-        raise ValueError(f"slots must have {n} elements, got {slots.shape[0]}")
-
-
-def _stream(cache: KVCache) -> int:
-    return torch.cuda.current_stream(cache.device).cuda_stream
+def _ids(t, name: str, cache: KVCache, dim: int, dtype: torch.dtype = _I32):
+    """A contiguous tensor of indices on the cache's GPU."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == dim and t.device == cache.device \
+            and t.is_cuda and t.is_contiguous():
+        return
+    _need(t, name)
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, expected {cache.device}")
+    raise TypeError(f"{name} must be {dtype} with {dim} dimension{'s' if dim > 1 else ''}")
 
 
 def write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
@@ -139,22 +141,24 @@ def write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor)
     n = k.shape[0]
     if v.shape[0] != n:
         raise ValueError(f"v must have {n} tokens, got {v.shape[0]}")
-    _slots(slots, cache, n)
+    _ids(slots, "slots", cache, 1, _INT64)
+    if slots.shape[0] != n:
+        raise ValueError(f"slots must have {n} elements, got {slots.shape[0]}")
     _check(lib().nvfp4_kv_write(cache._ref, k.data_ptr(), v.data_ptr(), dt, n, k_ts, k_hs,
-                                v_ts, v_hs, slots.data_ptr(), _stream(cache)), "nvfp4_kv_write")
+                                v_ts, v_hs, slots.data_ptr(), _raw_stream(cache._index)), "nvfp4_kv_write")
 
 
 def read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16):
     """Keys and values [n, kv_heads, head_dim] of the slots [n] (int64), dequantised to `dtype`;
     zeros for slots outside the cache."""
-    _slots(slots, cache)
-    if dtype not in (torch.float32, torch.bfloat16):
+    _ids(slots, "slots", cache, 1, _INT64)
+    if dtype is not _BF16 and dtype is not _F32:
         raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
     n = slots.shape[0]
-    k = torch.empty(n, cache.kv_heads, cache.head_dim, dtype=dtype, device=cache.device)
+    k = torch.empty((n, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
     v = torch.empty_like(k)
     _check(lib().nvfp4_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _dt(k),
-                               _stream(cache)), "nvfp4_kv_read")
+                               _raw_stream(cache._index)), "nvfp4_kv_read")
     return k, v
 
 
@@ -164,14 +168,6 @@ def attention_workspace_size(cache: KVCache, dtype: torch.dtype, tokens: int, he
     dt = nvfp4.DTYPE_BF16 if dtype == torch.bfloat16 else nvfp4.DTYPE_F32
     return int(lib().nvfp4_kv_attention_workspace_size(cache._ref, dt, tokens, heads, batch, max_q,
                                                        max_kv, prefix_len))
-
-
-def _ids(t, name: str, cache: KVCache, dim: int):
-    _need(t, name)
-    if t.device != cache.device:
-        raise ValueError(f"{name} is on {t.device}, expected {cache.device}")
-    if t.dtype != torch.int32 or t.dim() != dim:
-        raise TypeError(f"{name} must be int32 with {dim} dimension{'s' if dim > 1 else ''}")
 
 
 def attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor | None = None,
@@ -253,5 +249,5 @@ def attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor | None 
         hd ** -0.5 if scale is None else scale, int(causal), out.data_ptr(),
         None if lse is None else lse.data_ptr(),
         None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), _stream(cache)), "nvfp4_kv_attention")
+        0 if workspace is None else workspace.numel(), _raw_stream(cache._index)), "nvfp4_kv_attention")
     return (out, lse) if return_lse else out
