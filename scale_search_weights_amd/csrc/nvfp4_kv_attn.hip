@@ -35,6 +35,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 #ifndef ROWS_OCC
 #define ROWS_OCC 1
 #endif
+#ifndef SCHED_BARRIER
+#define SCHED_BARRIER __builtin_amdgcn_sched_barrier(0);
+#endif
 #ifndef WANT_TILE
 #define WANT_TILE 512
 #endif
@@ -153,7 +156,7 @@ __device__ __forceinline__ bool share_of(const Attn &p, int lane, Share &s) {
   const int slot = w % p.slots;
   w /= p.slots;
   s.h = w % p.kv_heads;
-  s.rt = w / p.kv_heads;
+  s.rt = p.row_tiles - 1 - w / p.kv_heads;  // the tiles that see most tokens first
   s.direct = p.direct;
   if (p.prefix || p.target == 0.0f) {
     s.j = job_of(p, p.prefix ? 0 : slot);
@@ -205,9 +208,32 @@ struct Tile {
   int ok;                                 // bit u: half u lies in a page of the cache
 };
 
+// Page ids of a token range, read ahead: lane k holds the id of the k-th group of 16 tokens of a
+// run of 1024, so a tile takes its ids from registers and no load waits for another.
+struct Pages {
+  int t0, run;    // the range's first token; the run in ids
+  int ids, next;  // this run's, the next one's
+};
+
+__device__ __forceinline__ int load_ids(const Attn &p, const Job &j, int t, int t_end, int lane) {
+  t += 16 * lane;
+  return t < t_end ? j.pages[t >> p.page_shift] : -1;
+}
+
+__device__ __forceinline__ Pages open_pages(const Attn &p, const Job &j, int t0, int t_end, int lane) {
+  return {t0, 0, load_ids(p, j, t0, t_end, lane), load_ids(p, j, t0 + 1024, t_end, lane)};
+}
+
+// Tiles are asked for in ascending order.
 template <int HD, bool EXACT>
-__device__ __forceinline__ void load_tile(const Attn &p, const Job &j, int h, int t, int t_end,
-                                          int lane, Tile<HD> &x) {
+__device__ __forceinline__ void load_tile(const Attn &p, const Job &j, Pages &pg, int h, int t,
+                                          int t_end, int lane, Tile<HD> &x) {
+  const int run = (t - pg.t0) >> 10;
+  if (run != pg.run) {
+    pg.run = run;
+    pg.ids = pg.next;
+    pg.next = load_ids(p, j, pg.t0 + 1024 * (run + 1), t_end, lane);
+  }
   const int i = lane & 15, quad = lane >> 4;
   const int nb = EXACT ? HD / 16 : p.hd >> 4;  // blocks of a row
   int64_t row[2];
@@ -215,13 +241,9 @@ __device__ __forceinline__ void load_tile(const Attn &p, const Job &j, int h, in
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int tb = t + 16 * u;
-    int id = 0;
-    if (tb < t_end) {
-      id = j.pages[tb >> p.page_shift];
-      if (id >= 0 && id < p.pages) x.ok |= 1 << u;
-      else id = 0;
-    }
-    // rows of a half that is not there are read from page 0 and never used
+    int id = __builtin_amdgcn_readlane(pg.ids, ((t - pg.t0) >> 4 & 63) + u);
+    if (id >= 0 && id < p.pages) x.ok |= 1 << u;
+    else id = 0;  // rows of a half that is not there are read from page 0 and never used
     row[u] = ((int64_t)id * p.kv_heads + h) << p.page_shift;
     row[u] += tb & ((1 << p.page_shift) - 1);
   }
@@ -538,10 +560,11 @@ __global__ void __launch_bounds__(256, ROWS_OCC) k_kv_attn_rows(Attn p) {
   t1 = min(t1, lim_hi);
 
   Tile<HD> cur, nxt;
+  Pages pg = open_pages(p, j, t0, t1, lane);
   int t = t0 + 32 * wave;
-  if (t < t1) load_tile<HD, EXACT>(p, j, h, t, t1, lane, cur);
+  if (t < t1) load_tile<HD, EXACT>(p, j, pg, h, t, t1, lane, cur);
   for (; t < t1; t += 128) {
-    if (t + 128 < t1) load_tile<HD, EXACT>(p, j, h, t + 128, t1, lane, nxt);
+    if (t + 128 < t1) load_tile<HD, EXACT>(p, j, pg, h, t + 128, t1, lane, nxt);
     stage_value_scales<HD>(cur, lane, vs_lds[wave]);
     f4 s[NT][2];
 #pragma unroll
@@ -672,9 +695,10 @@ __global__ void __launch_bounds__(256, PER_SIMD) k_kv_attn_tile(Attn p) {
   if (r0 >= rows) lim_hi = 0;  // a wave without rows only dequantises
 
   Tile<HD> cur, nxt;
-  if (t0 < t1) load_tile<HD, EXACT>(p, j, h, t0 + 32 * wave, t1, lane, cur);
+  Pages pg = open_pages(p, j, t0, t1, lane);
+  if (t0 < t1) load_tile<HD, EXACT>(p, j, pg, h, t0 + 32 * wave, t1, lane, cur);
   for (int t = t0; t < t1; t += 128) {
-    if (t + 128 < t1) load_tile<HD, EXACT>(p, j, h, t + 128 + 32 * wave, t1, lane, nxt);
+    if (t + 128 < t1) load_tile<HD, EXACT>(p, j, pg, h, t + 128 + 32 * wave, t1, lane, nxt);
     stage_value_scales<HD>(cur, lane, vs_lds[wave]);
     if (t > t0) __syncthreads();  // the last stage has been read
     if (lane == 0) oks[wave] = cur.ok;
@@ -695,38 +719,47 @@ __global__ void __launch_bounds__(256, PER_SIMD) k_kv_attn_tile(Attn p) {
       for (int d = 0; d < C; ++d) vfrag[wave][8 * word + d][lane] = a[d];
     }
     __syncthreads();
+    // operands are read one step ahead of their products: the values' before the exponentials,
+    // the next tile's keys before the second product
+    h8 kf[2 * KS];
+#pragma unroll
+    for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[0][k][lane];
 #pragma unroll 1
     for (int k4 = 0; k4 < 4; ++k4) {
       const int tt = t + 32 * k4;
       if (tt >= t1 || tt >= lim_hi) break;
       f4 s[NT][2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = (f4){0, 0, 0, 0};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) s[n][u] = (f4){0, 0, 0, 0};
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const h8 a = kfrag[k4][u * KS + k][lane];
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int q = 0; q < HALVES; ++q)
-              s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, x.q[n][q][k], s[n][u], 0, 0, 0);
-        }
-      }
+              s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u * KS + k], x.q[n][q][k], s[n][u], 0, 0, 0);
+      h8 vf[DV];
+#pragma unroll
+      for (int d = 0; d < DV; ++d) vf[d] = vfrag[k4][d][lane];
       const int ok = __builtin_amdgcn_readfirstlane(oks[k4]);
+      SCHED_BARRIER
       if (tt + 32 > lim_lo || ok != 3) hide<NT>(s, x.lim, tt, t1, ok, quad);
       h8 pf[NT][HALVES];
       probabilities<HD, NT, F32>(s, x, pf);
+      if (k4 < 3) {
 #pragma unroll
-      for (int d = 0; d < DV; ++d) {
-        const h8 a = vfrag[k4][d][lane];
+        for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[k4 + 1][k][lane];
+      }
+      SCHED_BARRIER
+#pragma unroll
+      for (int d = 0; d < DV; ++d)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int q = 0; q < HALVES; ++q)
-            x.acc[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf[n][q], x.acc[n][d], 0, 0, 0);
-      }
+            x.acc[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], pf[n][q], x.acc[n][d], 0, 0, 0);
     }
     cur = nxt;
   }
