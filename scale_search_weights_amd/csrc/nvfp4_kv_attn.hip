@@ -35,15 +35,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 #ifndef ROWS_OCC
 #define ROWS_OCC 1
 #endif
-#ifndef SCHED_BARRIER
-#define SCHED_BARRIER __builtin_amdgcn_sched_barrier(0);
-#endif
-#ifndef WANT_TILE
-#define WANT_TILE 512
+#ifndef TILE_W
+#define TILE_W 8
 #endif
 #ifndef TILE_NT
 #define TILE_NT 2
-#define TILE_OCC 2
 #endif
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -197,19 +193,21 @@ __device__ __forceinline__ float row_factor(float amax, float &inverse) {
   return __uint_as_float((unsigned)(127 + e) << 23);
 }
 
-// ---------------------------------------------------------------- raw tiles of 32 tokens
+// ---------------------------------------------------------------- raw groups of 16 tokens
 
+constexpr int more(int a) { return a > 1 ? a : 1; }
+
+// One lane's share of 16 tokens of one head, as cached. A group lies in one page.
 template <int HD>
-struct Tile {
-  unsigned k[2][HD / 32];                 // lane's HD/4 key codes of token i, two 16-token halves
-  unsigned ks[2];                         // their HD/64 scale bytes
-  unsigned v[8][HD > 128 ? HD / 128 : 1]; // lane's HD/16 value codes of its eight tokens
-  unsigned vs[HD > 128 ? HD / 128 : 1];   // HD/32 value scale bytes of token lane / 2
-  int ok;                                 // bit u: half u lies in a page of the cache
+struct Group {
+  unsigned k[HD / 32];             // HD/4 key codes of token i, from channel quad HD/4
+  unsigned ks;                     // their HD/64 scale bytes
+  unsigned v[4][more(HD / 128)];   // HD/16 value codes of tokens 4 quad + 0..3, from channel i HD/16
+  unsigned vs;                     // HD/64 value scale bytes of token lane / 4
 };
 
-// Page ids of a token range, read ahead: lane k holds the id of the k-th group of 16 tokens of a
-// run of 1024, so a tile takes its ids from registers and no load waits for another.
+// Page ids of a token range, read ahead: lane k holds the id of the k-th group of a run of 1024
+// tokens, so a group takes its id from a register and no load waits for another.
 struct Pages {
   int t0, run;    // the range's first token; the run in ids
   int ids, next;  // this run's, the next one's
@@ -224,157 +222,145 @@ __device__ __forceinline__ Pages open_pages(const Attn &p, const Job &j, int t0,
   return {t0, 0, load_ids(p, j, t0, t_end, lane), load_ids(p, j, t0 + 1024, t_end, lane)};
 }
 
-// Tiles are asked for in ascending order.
-template <int HD, bool EXACT>
-__device__ __forceinline__ void load_tile(const Attn &p, const Job &j, Pages &pg, int h, int t,
-                                          int t_end, int lane, Tile<HD> &x) {
+// The page of the group at t; runs are asked for in ascending order.
+__device__ __forceinline__ int page_of(const Attn &p, const Job &j, Pages &pg, int t, int t_end, int lane) {
   const int run = (t - pg.t0) >> 10;
   if (run != pg.run) {
     pg.run = run;
     pg.ids = pg.next;
     pg.next = load_ids(p, j, pg.t0 + 1024 * (run + 1), t_end, lane);
   }
+  return __builtin_amdgcn_readlane(pg.ids, (t - pg.t0) >> 4 & 63);
+}
+
+// Loads the group at t of page `id`; returns whether the page is one of the cache's. A group
+// that is not there is read from page 0 and never used.
+template <int HD, bool EXACT>
+__device__ __forceinline__ int load_group(const Attn &p, int id, int h, int t, int lane, Group<HD> &x) {
   const int i = lane & 15, quad = lane >> 4;
   const int nb = EXACT ? HD / 16 : p.hd >> 4;  // blocks of a row
-  int64_t row[2];
-  x.ok = 0;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int tb = t + 16 * u;
-    int id = __builtin_amdgcn_readlane(pg.ids, ((t - pg.t0) >> 4 & 63) + u);
-    if (id >= 0 && id < p.pages) x.ok |= 1 << u;
-    else id = 0;  // rows of a half that is not there are read from page 0 and never used
-    row[u] = ((int64_t)id * p.kv_heads + h) << p.page_shift;
-    row[u] += tb & ((1 << p.page_shift) - 1);
-  }
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const uint8_t *kc = p.kc + row[u] * (nb * 8), *ks = p.ks + row[u] * nb;
-    const uint8_t *vc = p.vc + row[u] * (nb * 8);
-    if (EXACT) {
-      const unsigned *k = reinterpret_cast<const unsigned *>(kc + i * (nb * 8) + quad * (HD / 8));
-      if constexpr (HD == 64) {
-        const uint2 a = *reinterpret_cast<const uint2 *>(k);
-        x.k[u][0] = a.x, x.k[u][1] = a.y;
-        x.ks[u] = ks[i * nb + quad];
-      } else {
-#pragma unroll
-        for (int w = 0; w < HD / 128; ++w) {
-          const uint4 a = *reinterpret_cast<const uint4 *>(k + 4 * w);
-          x.k[u][4 * w] = a.x, x.k[u][4 * w + 1] = a.y, x.k[u][4 * w + 2] = a.z, x.k[u][4 * w + 3] = a.w;
-        }
-        if constexpr (HD == 128) x.ks[u] = *reinterpret_cast<const uint16_t *>(ks + i * nb + 2 * quad);
-        else x.ks[u] = *reinterpret_cast<const unsigned *>(ks + i * nb + 4 * quad);
-      }
-    } else {
-      x.ks[u] = 0;
-#pragma unroll
-      for (int w = 0; w < HD / 64; ++w) {
-        const int b = quad * (HD / 64) + w;
-        uint2 a = make_uint2(0, 0);
-        if (b < nb) {
-          a = *reinterpret_cast<const uint2 *>(kc + (i * nb + b) * 8);
-          x.ks[u] |= (unsigned)ks[i * nb + b] << (8 * w);
-        }
-        x.k[u][2 * w] = a.x, x.k[u][2 * w + 1] = a.y;
-      }
-    }
-    const bool in = EXACT || i * (HD / 16) < p.hd;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint8_t *v = vc + (4 * quad + e) * (nb * 8) + i * (HD / 32);
-      unsigned *to = x.v[4 * u + e];
-      to[0] = 0;
-      if constexpr (HD > 128) to[1] = 0;
-      if (in) {
-        if constexpr (HD == 64) to[0] = *reinterpret_cast<const uint16_t *>(v);
-        else if constexpr (HD == 128) to[0] = *reinterpret_cast<const unsigned *>(v);
-        else {
-          const uint2 a = *reinterpret_cast<const uint2 *>(v);
-          to[0] = a.x, to[1] = a.y;
-        }
-      }
-    }
-  }
-  // value scales: lane / 2 is the token, each lane half of its blocks
-  const int64_t vrow = (lane < 32 ? row[0] : row[1]) + ((lane >> 1) & 15);
-  const uint8_t *vs = p.vs + vrow * nb;
+  const int ok = id >= 0 && id < p.pages;
+  const int64_t row = (((int64_t)(ok ? id : 0) * p.kv_heads + h) << p.page_shift) +
+                      (t & ((1 << p.page_shift) - 1));
+  const uint8_t *kc = p.kc + row * (nb * 8), *ks = p.ks + row * nb;
+  const uint8_t *vc = p.vc + row * (nb * 8), *vs = p.vs + row * nb;
   if (EXACT) {
-    vs += (lane & 1) * (HD / 32);
-    if constexpr (HD == 64) x.vs[0] = *reinterpret_cast<const uint16_t *>(vs);
-    else if constexpr (HD == 128) x.vs[0] = *reinterpret_cast<const unsigned *>(vs);
-    else {
-      const uint2 a = *reinterpret_cast<const uint2 *>(vs);
-      x.vs[0] = a.x, x.vs[1] = a.y;
+    const unsigned *k = reinterpret_cast<const unsigned *>(kc + i * (nb * 8) + quad * (HD / 8));
+    if constexpr (HD == 64) {
+      const uint2 a = *reinterpret_cast<const uint2 *>(k);
+      x.k[0] = a.x, x.k[1] = a.y;
+    } else {
+#pragma unroll
+      for (int w = 0; w < HD / 128; ++w) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(k + 4 * w);
+        x.k[4 * w] = a.x, x.k[4 * w + 1] = a.y, x.k[4 * w + 2] = a.z, x.k[4 * w + 3] = a.w;
+      }
+    }
+    ks += i * nb + quad * (HD / 64), vs += (lane >> 2) * nb + (lane & 3) * (HD / 64);
+    if constexpr (HD == 64) {
+      x.ks = *ks, x.vs = *vs;
+    } else if constexpr (HD == 128) {
+      x.ks = *reinterpret_cast<const uint16_t *>(ks), x.vs = *reinterpret_cast<const uint16_t *>(vs);
+    } else {
+      x.ks = *reinterpret_cast<const unsigned *>(ks), x.vs = *reinterpret_cast<const unsigned *>(vs);
     }
   } else {
+    x.ks = x.vs = 0;
 #pragma unroll
-    for (int w = 0; w < (HD > 128 ? HD / 128 : 1); ++w) x.vs[w] = 0;
-#pragma unroll
-    for (int w = 0; w < HD / 32; ++w) {
-      const int b = (lane & 1) * (HD / 32) + w;
-      if (b < nb) x.vs[w >> 2] |= (unsigned)vs[b] << (8 * (w & 3));
+    for (int w = 0; w < HD / 64; ++w) {
+      const int b = quad * (HD / 64) + w, c = (lane & 3) * (HD / 64) + w;
+      uint2 a = make_uint2(0, 0);
+      if (b < nb) {
+        a = *reinterpret_cast<const uint2 *>(kc + (i * nb + b) * 8);
+        x.ks |= (unsigned)ks[i * nb + b] << (8 * w);
+      }
+      x.k[2 * w] = a.x, x.k[2 * w + 1] = a.y;
+      if (c < nb) x.vs |= (unsigned)vs[(lane >> 2) * nb + c] << (8 * w);
     }
   }
+  const bool in = EXACT || i * (HD / 16) < p.hd;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint8_t *v = vc + (4 * quad + e) * (nb * 8) + i * (HD / 32);
+    x.v[e][0] = 0;
+    if constexpr (HD > 128) x.v[e][1] = 0;
+    if (in) {
+      if constexpr (HD == 64) x.v[e][0] = *reinterpret_cast<const uint16_t *>(v);
+      else if constexpr (HD == 128) x.v[e][0] = *reinterpret_cast<const unsigned *>(v);
+      else {
+        const uint2 a = *reinterpret_cast<const uint2 *>(v);
+        x.v[e][0] = a.x, x.v[e][1] = a.y;
+      }
+    }
+  }
+  return ok;
 }
 
-// Key operand of contraction step s for one 16-token half: eight channels of the lane's token.
+// Key operands of a group: out[s] holds eight channels of the lane's token, contraction step s.
 template <int HD>
-__device__ __forceinline__ h8 key_step(const Tile<HD> &x, int u, int s, const h2 *ksc) {
-  const h2 two = ksc[s >> 2];
-  const _Float16 f = (s >> 1) & 1 ? two[1] : two[0];
-  const h2 sc = {f, f};
-  const unsigned w = x.k[u][s];
-  union { h8 v; h2 p[4]; } r;
+__device__ __forceinline__ void key_frags(const Group<HD> &x, h8 *out) {
+  h2 sc[more(HD / 128)];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) r.p[b] = codes2(w, b) * sc;
-  return r.v;
-}
-
-// Value scales of a tile as fp16, transposed through LDS to [block][token]: 36 halves a row so
-// that the eight-byte reads of a half wave fall on different banks.
-constexpr int kVsRow = 36;
-
-template <int HD>
-__device__ __forceinline__ void stage_value_scales(const Tile<HD> &x, int lane, _Float16 *lds) {
-  const int tok = lane >> 1, b0 = (lane & 1) * (HD / 32);
+  for (int k = 0; k < more(HD / 128); ++k) sc[k] = scales2(x.ks, k);
 #pragma unroll
-  for (int w = 0; w < HD / 64; ++w) {
-    const h2 s = scales2(x.vs[w >> 1], w & 1);
-    lds[(b0 + 2 * w) * kVsRow + tok] = s[0];
-    lds[(b0 + 2 * w + 1) * kVsRow + tok] = s[1];
+  for (int s = 0; s < HD / 32; ++s) {
+    const _Float16 f = (s >> 1) & 1 ? sc[s >> 2][1] : sc[s >> 2][0];
+    const h2 two = {f, f};
+    union { h8 v; h2 p[4]; } r;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) r.p[b] = codes2(x.k[s], b) * two;
+    out[s] = r.v;
   }
 }
 
-// Value operands: out[c] holds channel i HD/16 + c of the lane's eight tokens. The codes of
-// two tokens are interleaved nibble by nibble first, so that one convert gives a pair of
-// tokens of one channel.
+// Value scales of a group as fp16, transposed through LDS to [block][token]: 20 halves a row so
+// that the eight-byte reads of a half wave fall on different banks.
+constexpr int kVsRow = 20;
+
 template <int HD>
-__device__ __forceinline__ void value_frags(const Tile<HD> &x, int lane, const _Float16 *lds,
-                                            int word, h8 *out) {
-  const int i = lane & 15, quad = lane >> 4;
-  // the scales come from other lanes of the wave: order the reads after their writes
+__device__ __forceinline__ void stage_value_scales(const Group<HD> &x, int lane, _Float16 *lds) {
+  const int tok = lane >> 2, b0 = (lane & 3) * (HD / 64);
+#pragma unroll
+  for (int w = 0; w < more(HD / 128); ++w) {
+    const h2 s = scales2(x.vs, w);
+    lds[(b0 + 2 * w) * kVsRow + tok] = s[0];
+    if (HD > 64) lds[(b0 + 2 * w + 1) * kVsRow + tok] = s[1];
+  }
+}
+
+__device__ __forceinline__ void order_wave_lds() {
+  // data from other lanes of the wave: order the reads after their writes
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-  const _Float16 *row = lds + ((i * (HD / 16)) >> 4) * kVsRow + 4 * quad;
-  const h4 s0 = *reinterpret_cast<const h4 *>(row), s1 = *reinterpret_cast<const h4 *>(row + 16);
-  const h2 sc[4] = {{s0[0], s0[1]}, {s0[2], s0[3]}, {s1[0], s1[1]}, {s1[2], s1[3]}};
+}
+
+// Value operands of a group: out[c] holds channel i HD/16 + c of the lane's four tokens. The
+// codes of two tokens are interleaved nibble by nibble first, so that one convert gives a
+// pair of tokens of one channel.
+template <int HD>
+__device__ __forceinline__ void value_frags(const Group<HD> &x, int lane, const _Float16 *lds, h4 *out) {
+  const int i = lane & 15, quad = lane >> 4;
+  const h4 s = *reinterpret_cast<const h4 *>(lds + ((i * (HD / 16)) >> 4) * kVsRow + 4 * quad);
+  const h2 sc[2] = {{s[0], s[1]}, {s[2], s[3]}};
   constexpr int C = HD >= 128 ? 8 : HD / 16;  // channels of a word
-  union { h8 v; h2 p[4]; } r[C];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const unsigned a = x.v[2 * e][word], b = x.v[2 * e + 1][word];
-    const unsigned even = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
-    const unsigned odd = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+  for (int word = 0; word < more(HD / 128); ++word) {
+    union { h4 v; h2 p[2]; } r[C];
 #pragma unroll
-    for (int c = 0; c < C; c += 2) {
-      r[c].p[e] = codes2(even, c >> 1) * sc[e];
-      r[c + 1].p[e] = codes2(odd, c >> 1) * sc[e];
+    for (int e = 0; e < 2; ++e) {
+      const unsigned a = x.v[2 * e][word], b = x.v[2 * e + 1][word];
+      const unsigned even = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+      const unsigned odd = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+#pragma unroll
+      for (int c = 0; c < C; c += 2) {
+        r[c].p[e] = codes2(even, c >> 1) * sc[e];
+        r[c + 1].p[e] = codes2(odd, c >> 1) * sc[e];
+      }
     }
-  }
 #pragma unroll
-  for (int c = 0; c < C; ++c) out[c] = r[c].v;
+    for (int c = 0; c < C; ++c) out[8 * word + c] = r[c].v;
+  }
 }
 
 template <bool F32>
@@ -541,7 +527,7 @@ __global__ void __launch_bounds__(256, ROWS_OCC) k_kv_attn_rows(Attn p) {
   constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, OROW = HD + 4;
   constexpr float kBase = base_of(F32);
   __shared__ __align__(16) float smem[4 * 16 * OROW];
-  __shared__ __align__(16) _Float16 vs_lds[4][DV * kVsRow];
+  __shared__ __align__(16) _Float16 vs_lds[4][2][DV * kVsRow];
   __shared__ float sm_m[4][16 * NT], sm_l[4][16 * NT];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -559,49 +545,58 @@ __global__ void __launch_bounds__(256, ROWS_OCC) k_kv_attn_rows(Attn p) {
   row_limits(p, j, r0, min(r0 + 16 * NT, rows), lim_lo, lim_hi);
   t1 = min(t1, lim_hi);
 
-  Tile<HD> cur, nxt;
+  Group<HD> cur[2], nxt[2];
+  int ok = 0, nxt_ok = 0;
   Pages pg = open_pages(p, j, t0, t1, lane);
   int t = t0 + 32 * wave;
-  if (t < t1) load_tile<HD, EXACT>(p, j, pg, h, t, t1, lane, cur);
+  if (t < t1)
+    for (int u = 0; u < 2; ++u)
+      ok |= load_group<HD, EXACT>(p, page_of(p, j, pg, t + 16 * u, t1, lane), h, t + 16 * u, lane, cur[u]) << u;
   for (; t < t1; t += 128) {
-    if (t + 128 < t1) load_tile<HD, EXACT>(p, j, pg, h, t + 128, t1, lane, nxt);
-    stage_value_scales<HD>(cur, lane, vs_lds[wave]);
+    if (t + 128 < t1) {
+      nxt_ok = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int tt = t + 128 + 16 * u;
+        nxt_ok |= load_group<HD, EXACT>(p, page_of(p, j, pg, tt, t1, lane), h, tt, lane, nxt[u]) << u;
+      }
+    }
     f4 s[NT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      h2 ksc[HD / 128 > 0 ? HD / 128 : 1];
-#pragma unroll
-      for (int k = 0; k < (HD / 128 > 0 ? HD / 128 : 1); ++k) ksc[k] = scales2(cur.ks[u], k);
+      stage_value_scales<HD>(cur[u], lane, vs_lds[wave][u]);
+      h8 kf[HD / 32];
+      key_frags<HD>(cur[u], kf);
 #pragma unroll
       for (int n = 0; n < NT; ++n) s[n][u] = (f4){0, 0, 0, 0};
 #pragma unroll
-      for (int k = 0; k < HD / 32; ++k) {
-        const h8 a = key_step<HD>(cur, u, k, ksc);
+      for (int k = 0; k < HD / 32; ++k)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int q = 0; q < HALVES; ++q)
-            s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, x.q[n][q][k], s[n][u], 0, 0, 0);
-      }
+            s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[k], x.q[n][q][k], s[n][u], 0, 0, 0);
     }
-    if (t + 32 > lim_lo || cur.ok != 3) hide<NT>(s, x.lim, t, t1, cur.ok, quad);
+    order_wave_lds();
+    if (t + 32 > lim_lo || ok != 3) hide<NT>(s, x.lim, t, t1, ok, quad);
     h8 pf[NT][HALVES];
     probabilities<HD, NT, F32>(s, x, pf);
+    h4 v0[DV], v1[DV];
+    value_frags<HD>(cur[0], lane, vs_lds[wave][0], v0);
+    value_frags<HD>(cur[1], lane, vs_lds[wave][1], v1);
 #pragma unroll
-    for (int word = 0; word < (HD > 128 ? HD / 128 : 1); ++word) {
-      constexpr int C = HD >= 128 ? 8 : HD / 16;
-      h8 a[C];
-      value_frags<HD>(cur, lane, vs_lds[wave], word, a);
+    for (int d = 0; d < DV; ++d) {
+      const h8 a = __builtin_shufflevector(v0[d], v1[d], 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-      for (int d = 0; d < C; ++d)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int q = 0; q < HALVES; ++q)
-            x.acc[n][8 * word + d] =
-                __builtin_amdgcn_mfma_f32_16x16x32_f16(a[d], pf[n][q], x.acc[n][8 * word + d], 0, 0, 0);
+        for (int q = 0; q < HALVES; ++q)
+          x.acc[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf[n][q], x.acc[n][d], 0, 0, 0);
     }
-    cur = nxt;
+    order_wave_lds();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) cur[u] = nxt[u];
+    ok = nxt_ok;
   }
 
   // join the four waves
@@ -664,24 +659,26 @@ __global__ void __launch_bounds__(256, ROWS_OCC) k_kv_attn_rows(Attn p) {
   }
 }
 
-// Many query rows over one token list (a shared prefix, a prompt): the four waves of a
-// workgroup hold 16 NT rows each. A stage is 128 tokens: every wave dequantises one 32-token
-// tile into LDS, as ready MFMA operands in lane order (16 bytes a lane, no bank conflicts), and
-// all waves read all four tiles.
-template <int HD, int NT, bool F32, bool EXACT, int PER_SIMD>
-__global__ void __launch_bounds__(256, PER_SIMD) k_kv_attn_tile(Attn p) {
-  constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, KS = HD / 32;
+// Many query rows over one token list (a shared prefix, a prompt): each of W waves holds 16 NT
+// rows. A stage is 16 W tokens: every wave dequantises a group of 16 into LDS, as ready MFMA
+// operands in lane order (no bank conflicts), and all waves read all tiles. Two stages
+// are in LDS, so a wave may dequantise the next stage before or after its products of this
+// one: even waves do it before, odd ones after, and the two waves of a SIMD keep its vector
+// units and its matrix cores busy at the same time.
+template <int HD, int NT, bool F32, bool EXACT, int W>
+__global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
+  constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, KS = HD / 32, STAGE = 16 * W;
   constexpr float kBase = base_of(F32);
-  __shared__ h8 kfrag[4][2 * KS][64], vfrag[4][DV][64];
-  __shared__ __align__(16) _Float16 vs_lds[4][DV * kVsRow];
-  __shared__ int oks[4];
+  __shared__ h8 kfrag[2][W][KS][64], vfrag[2][W / 2][DV][64];
+  __shared__ __align__(16) _Float16 vs_lds[W][DV * kVsRow];
+  __shared__ int oks[2][W];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int i = lane & 15, quad = lane >> 4;
   Share sh;
   if (!share_of(p, lane, sh)) return;
   const Job j = sh.j;
-  const int h = sh.h, rows = j.nq * p.group, R0 = sh.rt * (64 * NT), t0 = sh.t0;
+  const int h = sh.h, rows = j.nq * p.group, R0 = sh.rt * (16 * NT * W), t0 = sh.t0;
   if (R0 >= rows) return;
   int t1 = sh.t1;
   const int r0 = R0 + wave * 16 * NT;
@@ -689,45 +686,56 @@ __global__ void __launch_bounds__(256, PER_SIMD) k_kv_attn_tile(Attn p) {
   Rows<HD, NT, F32> x;
   load_rows<HD, NT, F32, EXACT>(p, j, h, r0, rows, lane, x);
   int lim_lo, lim_hi, none;
-  row_limits(p, j, R0, min(R0 + 64 * NT, rows), none, lim_hi);
+  row_limits(p, j, R0, min(R0 + 16 * NT * W, rows), none, lim_hi);
   t1 = min(t1, lim_hi);
   row_limits(p, j, min(r0, rows - 1), min(r0 + 16 * NT, rows), lim_lo, lim_hi);
   if (r0 >= rows) lim_hi = 0;  // a wave without rows only dequantises
 
-  Tile<HD> cur, nxt;
+  Group<HD> g;
+  int ok = 0;
   Pages pg = open_pages(p, j, t0, t1, lane);
-  if (t0 < t1) load_tile<HD, EXACT>(p, j, pg, h, t0 + 32 * wave, t1, lane, cur);
-  for (int t = t0; t < t1; t += 128) {
-    if (t + 128 < t1) load_tile<HD, EXACT>(p, j, pg, h, t + 128 + 32 * wave, t1, lane, nxt);
-    stage_value_scales<HD>(cur, lane, vs_lds[wave]);
-    if (t > t0) __syncthreads();  // the last stage has been read
-    if (lane == 0) oks[wave] = cur.ok;
+  const auto fetch = [&](int t) {  // this wave's group of the stage at t
+    t += 16 * wave;
+    ok = load_group<HD, EXACT>(p, page_of(p, j, pg, t, t1, lane), h, t, lane, g);
+  };
+  const auto dequantise = [&](int b) {
+    stage_value_scales<HD>(g, lane, vs_lds[wave]);
+    if (lane == 0) oks[b][wave] = ok;
+    h8 kf[KS];
+    key_frags<HD>(g, kf);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      h2 ksc[HD / 128 > 0 ? HD / 128 : 1];
+    for (int k = 0; k < KS; ++k) kfrag[b][wave][k][lane] = kf[k];
+    order_wave_lds();
+    h4 vf[DV];
+    value_frags<HD>(g, lane, vs_lds[wave], vf);
 #pragma unroll
-      for (int k = 0; k < (HD / 128 > 0 ? HD / 128 : 1); ++k) ksc[k] = scales2(cur.ks[u], k);
-#pragma unroll
-      for (int k = 0; k < KS; ++k) kfrag[wave][u * KS + k][lane] = key_step<HD>(cur, u, k, ksc);
-    }
-#pragma unroll
-    for (int word = 0; word < (HD > 128 ? HD / 128 : 1); ++word) {
-      constexpr int C = HD >= 128 ? 8 : HD / 16;
-      h8 a[C];
-      value_frags<HD>(cur, lane, vs_lds[wave], word, a);
-#pragma unroll
-      for (int d = 0; d < C; ++d) vfrag[wave][8 * word + d][lane] = a[d];
-    }
-    __syncthreads();
+    for (int d = 0; d < DV; ++d)
+      reinterpret_cast<h4 *>(&vfrag[b][wave >> 1][d][lane])[wave & 1] = vf[d];
+    order_wave_lds();
+  };
+  if (t0 < t1) {
+    fetch(t0);
+    dequantise(0);
+    if (t0 + STAGE < t1) fetch(t0 + STAGE);
+  }
+  __syncthreads();
+  int b = 0;
+  for (int t = t0; t < t1; t += STAGE, b ^= 1) {
+    const bool more_stages = t + STAGE < t1;
+    const auto next = [&]() {
+      dequantise(b ^ 1);
+      if (t + 2 * STAGE < t1) fetch(t + 2 * STAGE);
+    };
+    if (more_stages && !(wave & 1)) next();
     // operands are read one step ahead of their products: the values' before the exponentials,
     // the next tile's keys before the second product
+    const int tiles = min(W / 2, (min(t1, lim_hi) - t + 31) >> 5);
     h8 kf[2 * KS];
 #pragma unroll
-    for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[0][k][lane];
+    for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[b][k / KS][k % KS][lane];
 #pragma unroll 1
-    for (int k4 = 0; k4 < 4; ++k4) {
-      const int tt = t + 32 * k4;
-      if (tt >= t1 || tt >= lim_hi) break;
+    for (int c = 0; c < tiles; ++c) {
+      const int tt = t + 32 * c;
       f4 s[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = (f4){0, 0, 0, 0};
@@ -742,17 +750,16 @@ __global__ void __launch_bounds__(256, PER_SIMD) k_kv_attn_tile(Attn p) {
               s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u * KS + k], x.q[n][q][k], s[n][u], 0, 0, 0);
       h8 vf[DV];
 #pragma unroll
-      for (int d = 0; d < DV; ++d) vf[d] = vfrag[k4][d][lane];
-      const int ok = __builtin_amdgcn_readfirstlane(oks[k4]);
-      SCHED_BARRIER
-      if (tt + 32 > lim_lo || ok != 3) hide<NT>(s, x.lim, tt, t1, ok, quad);
+      for (int d = 0; d < DV; ++d) vf[d] = vfrag[b][c][d][lane];
+      const int seen = __builtin_amdgcn_readfirstlane(oks[b][2 * c] | oks[b][2 * c + 1] << 1);
+      __builtin_amdgcn_sched_barrier(0);
+      if (tt + 32 > lim_lo || seen != 3) hide<NT>(s, x.lim, tt, t1, seen, quad);
       h8 pf[NT][HALVES];
       probabilities<HD, NT, F32>(s, x, pf);
-      if (k4 < 3) {
+      const int nc = min(c + 1, W / 2 - 1);
 #pragma unroll
-        for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[k4 + 1][k][lane];
-      }
-      SCHED_BARRIER
+      for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[b][2 * nc + k / KS][k % KS][lane];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int d = 0; d < DV; ++d)
 #pragma unroll
@@ -761,7 +768,8 @@ __global__ void __launch_bounds__(256, PER_SIMD) k_kv_attn_tile(Attn p) {
           for (int q = 0; q < HALVES; ++q)
             x.acc[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], pf[n][q], x.acc[n][d], 0, 0, 0);
     }
-    cur = nxt;
+    if (more_stages && (wave & 1)) next();
+    __syncthreads();
   }
 
   // each lane holds HD/16 consecutive channels of its row four times
@@ -885,7 +893,7 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
 namespace {
 
 struct Part {    // one launch: the prefix or the sequences' own tokens
-  int nt, tile;  // 16-row tiles of a wave; tile: k_kv_attn_tile instead of k_kv_attn_rows
+  int nt, waves;  // 16-row tiles of a wave; waves of k_kv_attn_tile, or 0 for k_kv_attn_rows
   int row_tiles, slots, piece;
   float target;
 };
@@ -900,10 +908,13 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 Part plan_rows(const KvAttention &a, int64_t rows) {
   Part r = {};
   const bool wide = a.cache->head_dim > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
-  r.tile = rows > 64;
-  if (r.tile) r.nt = wide || f32 ? 1 : TILE_NT;
-  else r.nt = rows <= 16 ? 1 : (rows <= 32 || wide || f32 ? 2 : 4);
-  r.row_tiles = (int)cdiv(rows, (r.tile ? 64 : 16) * r.nt);
+  if (rows > 64) {
+    r.nt = wide || f32 ? 1 : TILE_NT;
+    r.waves = wide || rows <= 64 * r.nt ? 4 : TILE_W;
+  } else {
+    r.nt = rows <= 16 ? 1 : (rows <= 32 || wide || f32 ? 2 : 4);
+  }
+  r.row_tiles = (int)cdiv(rows, 16 * r.nt * (r.waves ? r.waves : 1));
   return r;
 }
 
@@ -912,13 +923,13 @@ Plan plan_of(const KvAttention &a) {
   const int64_t G = a.heads / a.cache->kv_heads;
   if (a.prefix_len > 0) {
     Part &r = p.prefix = plan_rows(a, a.tokens * G);
-    const int64_t units = a.cache->kv_heads * r.row_tiles, want = r.tile ? WANT_TILE : WANT_ROWS;
+    const int64_t units = a.cache->kv_heads * r.row_tiles, want = r.waves ? 2048 / r.waves : WANT_ROWS;
     r.piece = (int)(cdiv(a.prefix_len, 128 * cdiv(want, units)) * 128);
     r.slots = (int)cdiv(a.prefix_len, r.piece);
   }
   if (a.max_kv > 0 || a.prefix_len == 0) {
     Part &r = p.own = plan_rows(a, a.max_q * G);
-    const int64_t units = a.cache->kv_heads * r.row_tiles, want = r.tile ? WANT_TILE : WANT_ROWS;
+    const int64_t units = a.cache->kv_heads * r.row_tiles, want = r.waves ? 2048 / r.waves : WANT_ROWS;
     const int64_t most = a.batch * cdiv(a.max_kv, 128);  // pieces of 128 tokens
     r.slots = (int)a.batch;
     if (a.max_kv > 128 && units < want) {
@@ -934,11 +945,14 @@ Plan plan_of(const KvAttention &a) {
 template <int HD, bool F32, bool EXACT>
 void launch_rows(const Attn &p, const Part &r, unsigned grid, hipStream_t st) {
   const dim3 g(grid), b(256);
-  if (r.tile) {
+  if (r.waves == 8) {
+    if constexpr (HD <= 128)
+      hipLaunchKernelGGL((k_kv_attn_tile<HD, F32 ? 1 : TILE_NT, F32, EXACT, 8>), g, dim3(512), 0, st, p);
+  } else if (r.waves == 4) {
     if constexpr (HD <= 128 && !F32)
-      hipLaunchKernelGGL((k_kv_attn_tile<HD, TILE_NT, F32, EXACT, TILE_OCC>), g, b, 0, st, p);
+      hipLaunchKernelGGL((k_kv_attn_tile<HD, TILE_NT, F32, EXACT, 4>), g, b, 0, st, p);
     else
-      hipLaunchKernelGGL((k_kv_attn_tile<HD, 1, F32, EXACT, 1>), g, b, 0, st, p);
+      hipLaunchKernelGGL((k_kv_attn_tile<HD, 1, F32, EXACT, 4>), g, b, 0, st, p);
   } else if (r.nt == 1) {
     hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT>), g, b, 0, st, p);
   } else if (r.nt == 2) {
