@@ -662,9 +662,10 @@ __global__ void __launch_bounds__(256, ROWS_OCC) k_kv_attn_rows(Attn p) {
 // Many query rows over one token list (a shared prefix, a prompt): each of W waves holds 16 NT
 // rows. A stage is 16 W tokens: every wave dequantises a group of 16 into LDS, as ready MFMA
 // operands in lane order (no bank conflicts), and all waves read all tiles. Two stages
-// are in LDS, so a wave may dequantise the next stage before or after its products of this
-// one: even waves do it before, odd ones after, and the two waves of a SIMD keep its vector
-// units and its matrix cores busy at the same time.
+// are in LDS, so the next one is dequantised beside the products of this one by whichever
+// wave comes to it. Score products run at a raised wave priority: of a SIMD's two waves, one in
+// its products then goes ahead of one in its exponentials, which fills the gaps between
+// them.
 template <int HD, int NT, bool F32, bool EXACT, int W>
 __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, KS = HD / 32, STAGE = 16 * W;
@@ -721,12 +722,6 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   __syncthreads();
   int b = 0;
   for (int t = t0; t < t1; t += STAGE, b ^= 1) {
-    const bool more_stages = t + STAGE < t1;
-    const auto next = [&]() {
-      dequantise(b ^ 1);
-      if (t + 2 * STAGE < t1) fetch(t + 2 * STAGE);
-    };
-    if (more_stages && !(wave & 1)) next();
     // operands are read one step ahead of their products: the values' before the exponentials,
     // the next tile's keys before the second product
     const int tiles = min(W / 2, (min(t1, lim_hi) - t + 31) >> 5);
@@ -736,6 +731,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
 #pragma unroll 1
     for (int c = 0; c < tiles; ++c) {
       const int tt = t + 32 * c;
+      __builtin_amdgcn_s_setprio(1);
       f4 s[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = (f4){0, 0, 0, 0};
@@ -752,6 +748,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
 #pragma unroll
       for (int d = 0; d < DV; ++d) vf[d] = vfrag[b][c][d][lane];
       const int seen = __builtin_amdgcn_readfirstlane(oks[b][2 * c] | oks[b][2 * c + 1] << 1);
+      __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
       if (tt + 32 > lim_lo || seen != 3) hide<NT>(s, x.lim, tt, t1, seen, quad);
       h8 pf[NT][HALVES];
@@ -768,7 +765,10 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
           for (int q = 0; q < HALVES; ++q)
             x.acc[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], pf[n][q], x.acc[n][d], 0, 0, 0);
     }
-    if (more_stages && (wave & 1)) next();
+    if (t + STAGE < t1) {
+      dequantise(b ^ 1);
+      if (t + 2 * STAGE < t1) fetch(t + 2 * STAGE);
+    }
     __syncthreads();
   }
 
