@@ -30,10 +30,10 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 #ifndef WANT_ROWS
-#define WANT_ROWS 768
+#define WANT_ROWS 1024
 #endif
-#ifndef ROWS_OCC
-#define ROWS_OCC 1
+#ifndef JT
+#define JT 256
 #endif
 #ifndef TILE_W
 #define TILE_W 8
@@ -60,6 +60,7 @@ struct Attn {
   void *out;
   float *lse, *opart;
   float2 *ml;
+  int2 *where;   // first slot and pieces of a sequence that has any
 };
 
 // One sequence's share of the call.
@@ -86,6 +87,22 @@ __device__ __forceinline__ Job job_of(const Attn &p, int b) {
   return j;
 }
 
+// Sums over the wave's lanes in six DPP steps: lane l gets the sum of lanes 0 .. l.
+template <int CTRL, int ROWS, typename T>
+__device__ __forceinline__ T dpp_add(T x) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, ROWS, 0xF, false);
+  return x + __builtin_bit_cast(T, o);
+}
+template <typename T>
+__device__ __forceinline__ T prefix_sum(T x) {
+  x = dpp_add<0x111, 0xF>(x);  // row_shr 1, 2, 4, 8
+  x = dpp_add<0x112, 0xF>(x);
+  x = dpp_add<0x114, 0xF>(x);
+  x = dpp_add<0x118, 0xF>(x);
+  x = dpp_add<0x142, 0xA>(x);  // row_bcast 15, 31
+  return dpp_add<0x143, 0xC>(x);
+}
+
 // The sequences' own tokens are cut into pieces of equal length, a multiple of 128 chosen from
 // the lengths found on the device so that about `target` pieces come out in all (at most
 // target + batch: every sequence may add one that is not full). Slots number the pieces over
@@ -99,34 +116,22 @@ __device__ __forceinline__ int units_of(const int32_t *kv_lens, int b, int max_l
   return (min(max(kv_lens[b], 0), max_len) + 127) >> 7;
 }
 
-__device__ __forceinline__ int piece_units(const int32_t *kv_lens, int batch, int max_len,
-                                           float target, int lane) {
+// The piece of `slot`; b = -1: there is none.
+__device__ __forceinline__ Piece find_piece(const int32_t *kv_lens, int batch, int max_len,
+                                            float target, int slot, int lane) {
   float sum = 0.0f;
   for (int b = lane; b < batch; b += 64) sum += (float)units_of(kv_lens, b, max_len);
-#pragma unroll
-  for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  sum = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(prefix_sum(sum)), 63));
   const float x = ceilf(sum / target);  // the same in every wave: same order, same bits
-  return __builtin_amdgcn_readfirstlane(x < 1.0f ? 1 : (x > 8388608.0f ? 8388608 : (int)x));
-}
-
-// The piece of `slot`, or (want_b >= 0) the slots of sequence want_b. b = -1: no such piece.
-__device__ __forceinline__ Piece find_piece(const int32_t *kv_lens, int batch, int max_len,
-                                            float target, int slot, int want_b, int lane) {
-  const int per = piece_units(kv_lens, batch, max_len, target, lane);
+  const int per = x < 1.0f ? 1 : (x > 8388608.0f ? 8388608 : (int)x);
   Piece r = {-1, 0, 0, per << 7};
   int before = 0;
   for (int b0 = 0; b0 < batch; b0 += 64) {
     const int b = b0 + lane;
     const int n = b < batch ? (units_of(kv_lens, b, max_len) + per - 1) / per : 0;
-    int upto = n;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(upto, off, 64);
-      if (lane >= off) upto += o;
-    }
-    const bool mine = want_b >= 0 ? b == want_b
-                                  : slot >= before + upto - n && slot < before + upto;
-    const unsigned long long hit = __ballot(mine);
+    const int upto = prefix_sum(n);
+    const unsigned long long hit =
+        __ballot(slot >= before + upto - n && slot < before + upto);
     if (hit) {
       const int at = __builtin_ctzll(hit);
       r.b = b0 + at;
@@ -159,8 +164,10 @@ __device__ __forceinline__ bool share_of(const Attn &p, int lane, Share &s) {
     s.t0 = p.prefix ? slot * p.piece : 0;
     s.t1 = p.prefix ? min(s.j.len, s.t0 + p.piece) : s.j.len;
   } else {
-    const Piece x = find_piece(p.kv_lens, p.batch, p.max_len, p.target, slot, -1, lane);
+    const Piece x = find_piece(p.kv_lens, p.batch, p.max_len, p.target, slot, lane);
     if (x.b < 0) return false;
+    if (slot == x.first && s.h == 0 && s.rt == 0 && threadIdx.x == 0)
+      p.where[x.b] = make_int2(x.first, x.count);  // for the join
     s.j = job_of(p, x.b);
     s.t0 = (slot - x.first) * x.tokens;
     s.t1 = min(s.j.len, s.t0 + x.tokens);
@@ -523,7 +530,7 @@ __device__ __forceinline__ void probabilities(f4 (*s)[2], Rows<HD, NT, F32> &x, 
 // Four waves take the 32-token tiles of a piece in turn, each for the same 16 NT query rows,
 // and join their sums at the end.
 template <int HD, int NT, bool F32, bool EXACT>
-__global__ void __launch_bounds__(256, ROWS_OCC) k_kv_attn_rows(Attn p) {
+__global__ void __launch_bounds__(256, NT == 1 && HD <= 128 && !F32 ? 4 : 1) k_kv_attn_rows(Attn p) {
   constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, OROW = HD + 4;
   constexpr float kBase = base_of(F32);
   __shared__ __align__(16) float smem[4 * 16 * OROW];
@@ -809,7 +816,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
 }
 
 // Join the partial sums of a row, one workgroup per (token, head): HD / 4 lanes take four
-// channels each, and the 1024 / HD groups of lanes take the row's pieces in turn. The
+// channels each, and the groups of lanes take the row's pieces in turn. The
 // prefix's pieces come first, then those of the sequence's own tokens.
 struct Join {
   const float *opart, *opart_own, *S_v;
@@ -817,16 +824,16 @@ struct Join {
   void *out;
   float *lse;
   const int32_t *q_offsets, *kv_lens;
-  int tokens, heads, kv_heads, group, hd, max_q, max_len, batch, n_prefix;
-  float target;
+  const int2 *where;  // NULL: one piece a sequence
+  int tokens, heads, kv_heads, group, hd, max_q, n_prefix;
 };
 
 template <int HD, bool F32>
-__global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
-  constexpr int LANES = HD / 4, GROUPS = 256 / LANES;
+__global__ void __launch_bounds__(JT) k_kv_attn_join(Join p) {
+  constexpr int LANES = HD / 4, GROUPS = JT / LANES;
   __shared__ f4 so[GROUPS][LANES];
   __shared__ float sm_m[GROUPS], sm_l[GROUPS];
-  const int lane = threadIdx.x & 63, b = blockIdx.y;
+  const int b = blockIdx.y;
   const int g = threadIdx.x / LANES, c = threadIdx.x % LANES;
   const int i = blockIdx.x / p.heads, head = blockIdx.x - i * p.heads;
   int lo = b * p.max_q, hi = lo + p.max_q;
@@ -836,9 +843,11 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
   }
   if (lo + i >= hi) return;
   int own0 = b, n = p.n_prefix;
-  if (p.target > 0.0f) {
-    const Piece x = find_piece(p.kv_lens, p.batch, p.max_len, p.target, 0, b, lane);
-    own0 = x.first, n += x.count;
+  if (p.where) {
+    if (p.kv_lens[b] > 0) {
+      const int2 x = p.where[b];
+      own0 = x.x, n += x.y;
+    }
   } else if (p.kv_lens) {
     n += 1;
   }
@@ -989,8 +998,8 @@ int64_t own_rows(const KvAttention &a, const Plan &p) {
 
 template <int HD>
 void launch_join(const Join &p, bool f32, dim3 g, hipStream_t st) {
-  if (f32) hipLaunchKernelGGL((k_kv_attn_join<HD, true>), g, dim3(256), 0, st, p);
-  else hipLaunchKernelGGL((k_kv_attn_join<HD, false>), g, dim3(256), 0, st, p);
+  if (f32) hipLaunchKernelGGL((k_kv_attn_join<HD, true>), g, dim3(JT), 0, st, p);
+  else hipLaunchKernelGGL((k_kv_attn_join<HD, false>), g, dim3(JT), 0, st, p);
 }
 
 }  // namespace
@@ -1003,7 +1012,7 @@ bool kv_attention_fits(const KvAttention &a) {
 size_t kv_attention_workspace_size(const KvAttention &a) {
   const Plan p = plan_of(a);
   if (p.direct) return 0;
-  return (size_t)((prefix_rows(a, p) + own_rows(a, p)) * (a.cache->head_dim * 4 + 8));
+  return (size_t)((prefix_rows(a, p) + own_rows(a, p)) * (a.cache->head_dim * 4 + 8) + a.batch * 8);
 }
 
 int launch_kv_attention(const KvAttention &a, hipStream_t st) {
@@ -1021,6 +1030,7 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
   p.out = a.out, p.lse = a.lse;
   float *opart = static_cast<float *>(a.workspace), *own = opart + n_pre * c.head_dim;
   float2 *ml = reinterpret_cast<float2 *>(own + n_own * c.head_dim), *ml_own = ml + n_pre;
+  int2 *where = reinterpret_cast<int2 *>(ml_own + n_own);
   const bool f32 = a.dtype == NVFP4_DTYPE_F32;
   if (plan.prefix.slots) {
     Attn x = p;
@@ -1036,7 +1046,7 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
     x.table = a.block_table, x.table_width = a.table_width, x.max_len = (int)a.max_kv;
     x.causal = a.causal, x.target = plan.own.target;
     x.slots = plan.own.slots, x.row_tiles = plan.own.row_tiles;
-    x.opart = own, x.ml = ml_own;
+    x.opart = own, x.ml = ml_own, x.where = where;
     const unsigned g = (unsigned)part_grid(a, plan.own);
     if (f32) launch_hd<true>(x, plan.own, g, st);
     else launch_hd<false>(x, plan.own, g, st);
@@ -1046,8 +1056,8 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
     x.opart = opart, x.opart_own = own, x.ml = ml, x.ml_own = ml_own;
     x.S_v = c.S_v, x.out = a.out, x.lse = a.lse, x.q_offsets = a.q_offsets, x.kv_lens = a.kv_lens;
     x.tokens = p.tokens, x.heads = p.heads, x.kv_heads = p.kv_heads, x.group = p.group, x.hd = p.hd;
-    x.max_q = p.max_q, x.max_len = (int)a.max_kv, x.batch = p.batch;
-    x.n_prefix = plan.prefix.slots, x.target = plan.own.target;
+    x.max_q = p.max_q, x.n_prefix = plan.prefix.slots;
+    x.where = plan.own.target > 0.0f ? where : nullptr;
     const dim3 g((unsigned)(a.max_q * a.heads), (unsigned)a.batch);
     if (p.hd <= 64) launch_join<64>(x, f32, g, st);
     else if (p.hd <= 128) launch_join<128>(x, f32, g, st);
