@@ -29,18 +29,6 @@ typedef float f2 __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
-#ifndef WANT_ROWS
-#define WANT_ROWS 1024
-#endif
-#ifndef JT
-#define JT 256
-#endif
-#ifndef TILE_W
-#define TILE_W 8
-#endif
-#ifndef TILE_NT
-#define TILE_NT 2
-#endif
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Attn {
@@ -57,6 +45,7 @@ struct Attn {
   float target;  // own tokens: pieces wanted in all; 0 for one piece a sequence
   int piece;     // prefix: tokens of a piece
   int direct;    // one piece a row, written straight to out
+  int joined;    // rows have prefix pieces too
   void *out;
   float *lse, *opart;
   float2 *ml;
@@ -103,13 +92,13 @@ __device__ __forceinline__ T prefix_sum(T x) {
   return dpp_add<0x143, 0xC>(x);
 }
 
-// The sequences' own tokens are cut into pieces of equal length, a multiple of 128 chosen from
-// the lengths found on the device so that about `target` pieces come out in all (at most
-// target + batch: every sequence may add one that is not full). Slots number the pieces over
+// The sequences' own tokens are cut into pieces of at most a length chosen from the lengths found
+// on the device so that about `target` pieces come out in all (at most target + batch: every
+// sequence may add one that is not full); a sequence's pieces are equal, in units of 128. Slots number the pieces over
 // all sequences, so the grid has few workgroups without work however unequal the lengths
 // are. Every wave finds its piece by itself: two passes over the lengths.
 struct Piece {
-  int b, first, count, tokens;  // sequence, its first slot, its pieces, tokens of a full piece
+  int b, first, count, tokens;  // sequence, its first slot, its pieces, tokens of each
 };
 
 __device__ __forceinline__ int units_of(const int32_t *kv_lens, int b, int max_len) {
@@ -124,7 +113,7 @@ __device__ __forceinline__ Piece find_piece(const int32_t *kv_lens, int batch, i
   sum = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(prefix_sum(sum)), 63));
   const float x = ceilf(sum / target);  // the same in every wave: same order, same bits
   const int per = x < 1.0f ? 1 : (x > 8388608.0f ? 8388608 : (int)x);
-  Piece r = {-1, 0, 0, per << 7};
+  Piece r = {-1, 0, 0, 0};
   int before = 0;
   for (int b0 = 0; b0 < batch; b0 += 64) {
     const int b = b0 + lane;
@@ -137,6 +126,8 @@ __device__ __forceinline__ Piece find_piece(const int32_t *kv_lens, int batch, i
       r.b = b0 + at;
       r.count = __builtin_amdgcn_readlane(n, at);
       r.first = before + __builtin_amdgcn_readlane(upto, at) - r.count;
+      const int units = units_of(kv_lens, r.b, max_len);
+      r.tokens = (units + r.count - 1) / r.count << 7;
       return r;
     }
     before += __builtin_amdgcn_readlane(upto, 63);
@@ -166,6 +157,7 @@ __device__ __forceinline__ bool share_of(const Attn &p, int lane, Share &s) {
   } else {
     const Piece x = find_piece(p.kv_lens, p.batch, p.max_len, p.target, slot, lane);
     if (x.b < 0) return false;
+    s.direct = x.count == 1 && !p.joined;  // the join skips such sequences
     if (slot == x.first && s.h == 0 && s.rt == 0 && threadIdx.x == 0)
       p.where[x.b] = make_int2(x.first, x.count);  // for the join
     s.j = job_of(p, x.b);
@@ -815,9 +807,9 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   }
 }
 
-// Join the partial sums of a row, one workgroup per (token, head): HD / 4 lanes take four
-// channels each, and the groups of lanes take the row's pieces in turn. The
-// prefix's pieces come first, then those of the sequence's own tokens.
+// Join the partial sums of the rows: HD / 4 lanes take four channels each; of a workgroup's
+// groups of such lanes `per` (a power of two, about the pieces of a row) share a row and take
+// its pieces in turn. The prefix's pieces come first, then those of the sequence's own tokens.
 struct Join {
   const float *opart, *opart_own, *S_v;
   const float2 *ml, *ml_own;
@@ -825,32 +817,34 @@ struct Join {
   float *lse;
   const int32_t *q_offsets, *kv_lens;
   const int2 *where;  // NULL: one piece a sequence
-  int tokens, heads, kv_heads, group, hd, max_q, n_prefix;
+  int tokens, heads, kv_heads, group, hd, max_q, n_prefix, per;
 };
 
 template <int HD, bool F32>
-__global__ void __launch_bounds__(JT) k_kv_attn_join(Join p) {
-  constexpr int LANES = HD / 4, GROUPS = JT / LANES;
+__global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
+  constexpr int LANES = HD / 4, GROUPS = 256 / LANES;
   __shared__ f4 so[GROUPS][LANES];
   __shared__ float sm_m[GROUPS], sm_l[GROUPS];
   const int b = blockIdx.y;
-  const int g = threadIdx.x / LANES, c = threadIdx.x % LANES;
-  const int i = blockIdx.x / p.heads, head = blockIdx.x - i * p.heads;
+  const int g = threadIdx.x / LANES, c = threadIdx.x % LANES, first = g & -p.per;
+  const int r = blockIdx.x * (GROUPS / p.per) + g / p.per;  // of the sequence: token, head
+  const int i = r / p.heads, head = r - i * p.heads;
   int lo = b * p.max_q, hi = lo + p.max_q;
   if (p.q_offsets) {
     lo = min(max(p.q_offsets[b], 0), p.tokens);
     hi = min(max(p.q_offsets[b + 1], lo), min(p.tokens, lo + p.max_q));
   }
-  if (lo + i >= hi) return;
   int own0 = b, n = p.n_prefix;
   if (p.where) {
     if (p.kv_lens[b] > 0) {
       const int2 x = p.where[b];
+      if (x.y == 1 && n == 0) return;  // written by its only piece
       own0 = x.x, n += x.y;
     }
   } else if (p.kv_lens) {
     n += 1;
   }
+  const bool here = lo + i < hi;
   const int h = head / p.group, gr = head - h * p.group;
   const int64_t rows = (int64_t)p.tokens * p.group, own_rows = (int64_t)p.max_q * p.group;
   const int64_t at = h * rows + (int64_t)(lo + i) * p.group + gr;      // in a prefix slot
@@ -859,8 +853,9 @@ __global__ void __launch_bounds__(JT) k_kv_attn_join(Join p) {
   float M = -INFINITY, L = 0.0f;
   f4 y = {0, 0, 0, 0};
   const bool in = 4 * c < p.hd;
+  if (!here) n = 0;
 #pragma unroll 4
-  for (int k = g; k < n; k += GROUPS) {
+  for (int k = g - first; k < n; k += p.per) {
     const bool pre = k < p.n_prefix;
     const int64_t row = pre ? at + k * step : own_at + (k - p.n_prefix) * own_step;
     const float2 ml = (pre ? p.ml : p.ml_own)[row];
@@ -877,16 +872,15 @@ __global__ void __launch_bounds__(JT) k_kv_attn_join(Join p) {
   if (c == 0) sm_m[g] = M, sm_l[g] = L;
   so[g][c] = y;
   __syncthreads();
-  if (g) return;
-  M = sm_m[0];
-  for (int k = 1; k < GROUPS; ++k) M = fmaxf(M, sm_m[k]);
+  if (g != first || !here) return;
+  for (int k = 1; k < p.per; ++k) M = fmaxf(M, sm_m[g + k]);
   L = 0.0f;
   y = (f4){0, 0, 0, 0};
-  for (int k = 0; k < GROUPS; ++k) {
-    if (!(sm_l[k] > 0.0f)) continue;
-    const float e = __builtin_amdgcn_exp2f(sm_m[k] - M);
-    L += sm_l[k] * e;
-    y += so[k][c] * e;
+  for (int k = 0; k < p.per; ++k) {
+    if (!(sm_l[g + k] > 0.0f)) continue;
+    const float e = __builtin_amdgcn_exp2f(sm_m[g + k] - M);
+    L += sm_l[g + k] * e;
+    y += so[g + k][c] * e;
   }
   const int64_t to = (int64_t)(lo + i) * p.heads + head;
   const float f = L > 0.0f ? p.S_v[h] / L : 0.0f;
@@ -901,9 +895,10 @@ __global__ void __launch_bounds__(JT) k_kv_attn_join(Join p) {
 
 namespace {
 
-struct Part {    // one launch: the prefix or the sequences' own tokens
-  int nt, waves;  // 16-row tiles of a wave; waves of k_kv_attn_tile, or 0 for k_kv_attn_rows
+struct Part {      // one launch: the prefix or the sequences' own tokens
+  int nt, waves;   // 16-row tiles of a wave; waves of k_kv_attn_tile, or 0 for k_kv_attn_rows
   int row_tiles, slots, piece;
+  int resident;    // workgroups that the chip holds at once
   float target;
 };
 
@@ -914,15 +909,24 @@ struct Plan {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Up to 32 rows a (sequence, key/value head): k_kv_attn_rows, whose waves work alone; more:
+// k_kv_attn_tile, whose waves share what they dequantise. Workgroups a CU holds: by registers
+// (HD and NT) for the first, by LDS (1 KiB a token at HD 256, two stages) for the second.
 Part plan_rows(const KvAttention &a, int64_t rows) {
   Part r = {};
-  const bool wide = a.cache->head_dim > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
-  if (rows > 64) {
-    r.nt = wide || f32 ? 1 : TILE_NT;
-    r.waves = wide || rows <= 64 * r.nt ? 4 : TILE_W;
+  const int64_t hd = a.cache->head_dim;
+  const bool wide = hd > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
+  int per_cu;
+  if (rows > 32) {
+    r.nt = wide || f32 || rows <= 64 ? 1 : 2;
+    r.waves = wide || rows <= 64 * r.nt ? 4 : 8;
+    per_cu = wide ? 1 : (hd > 64 || r.waves == 8 ? 8 / r.waves : 3);
   } else {
-    r.nt = rows <= 16 ? 1 : (rows <= 32 || wide || f32 ? 2 : 4);
+    r.nt = rows <= 16 ? 1 : 2;
+    const int one = wide ? (f32 ? 1 : 2) : (f32 ? 3 : 4);
+    per_cu = r.nt == 1 || one == 1 ? one : one / 2;
   }
+  r.resident = 256 * per_cu;
   r.row_tiles = (int)cdiv(rows, 16 * r.nt * (r.waves ? r.waves : 1));
   return r;
 }
@@ -932,18 +936,22 @@ Plan plan_of(const KvAttention &a) {
   const int64_t G = a.heads / a.cache->kv_heads;
   if (a.prefix_len > 0) {
     Part &r = p.prefix = plan_rows(a, a.tokens * G);
-    const int64_t units = a.cache->kv_heads * r.row_tiles, want = r.waves ? 2048 / r.waves : WANT_ROWS;
-    r.piece = (int)(cdiv(a.prefix_len, 128 * cdiv(want, units)) * 128);
+    const int64_t units = a.cache->kv_heads * r.row_tiles;
+    const int64_t n = units < r.resident ? r.resident / units : 1;
+    r.piece = (int)(cdiv(a.prefix_len, 128 * n) * 128);
     r.slots = (int)cdiv(a.prefix_len, r.piece);
   }
   if (a.max_kv > 0 || a.prefix_len == 0) {
     Part &r = p.own = plan_rows(a, a.max_q * G);
-    const int64_t units = a.cache->kv_heads * r.row_tiles, want = r.waves ? 2048 / r.waves : WANT_ROWS;
+    const int64_t units = a.cache->kv_heads * r.row_tiles;
     const int64_t most = a.batch * cdiv(a.max_kv, 128);  // pieces of 128 tokens
+    const float target = (float)r.resident / (float)units;
     r.slots = (int)a.batch;
-    if (a.max_kv > 128 && units < want) {
-      r.target = (float)want / (float)units;
-      const int64_t n = want / units + 1 + a.batch;
+    // many rows: a row's partial sums cost more than a workgroup's wait, so only where there
+    // are far fewer workgroups than the chip holds
+    if (a.max_kv > 128 && target >= (r.waves ? 1.5f * (float)a.batch : 1.0f)) {
+      r.target = target;
+      const int64_t n = (int64_t)target + 1 + a.batch;
       r.slots = (int)(n < most ? n : most);
     }
   }
@@ -956,18 +964,15 @@ void launch_rows(const Attn &p, const Part &r, unsigned grid, hipStream_t st) {
   const dim3 g(grid), b(256);
   if (r.waves == 8) {
     if constexpr (HD <= 128)
-      hipLaunchKernelGGL((k_kv_attn_tile<HD, F32 ? 1 : TILE_NT, F32, EXACT, 8>), g, dim3(512), 0, st, p);
+      hipLaunchKernelGGL((k_kv_attn_tile<HD, F32 ? 1 : 2, F32, EXACT, 8>), g, dim3(512), 0, st, p);
   } else if (r.waves == 4) {
-    if constexpr (HD <= 128 && !F32)
-      hipLaunchKernelGGL((k_kv_attn_tile<HD, TILE_NT, F32, EXACT, 4>), g, b, 0, st, p);
-    else
-      hipLaunchKernelGGL((k_kv_attn_tile<HD, 1, F32, EXACT, 4>), g, b, 0, st, p);
+    if (r.nt == 1) hipLaunchKernelGGL((k_kv_attn_tile<HD, 1, F32, EXACT, 4>), g, b, 0, st, p);
+    else if constexpr (HD <= 128 && !F32)
+      hipLaunchKernelGGL((k_kv_attn_tile<HD, 2, F32, EXACT, 4>), g, b, 0, st, p);
   } else if (r.nt == 1) {
     hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT>), g, b, 0, st, p);
-  } else if (r.nt == 2) {
+  } else {
     hipLaunchKernelGGL((k_kv_attn_rows<HD, 2, F32, EXACT>), g, b, 0, st, p);
-  } else if constexpr (HD <= 128 && !F32) {
-    hipLaunchKernelGGL((k_kv_attn_rows<HD, 4, F32, EXACT>), g, b, 0, st, p);
   }
 }
 
@@ -997,9 +1002,15 @@ int64_t own_rows(const KvAttention &a, const Plan &p) {
 }
 
 template <int HD>
-void launch_join(const Join &p, bool f32, dim3 g, hipStream_t st) {
-  if (f32) hipLaunchKernelGGL((k_kv_attn_join<HD, true>), g, dim3(JT), 0, st, p);
-  else hipLaunchKernelGGL((k_kv_attn_join<HD, false>), g, dim3(JT), 0, st, p);
+void launch_join(Join &p, const KvAttention &a, const Plan &plan, hipStream_t st) {
+  constexpr int GROUPS = 1024 / HD;
+  const float n = (float)plan.prefix.slots + plan.own.target / (float)a.batch;
+  p.per = 1;
+  while (p.per < GROUPS && (float)p.per < n) p.per *= 2;
+  const dim3 g((unsigned)cdiv(a.max_q * a.heads, GROUPS / p.per), (unsigned)a.batch);
+  const bool f32 = a.dtype == NVFP4_DTYPE_F32;
+  if (f32) hipLaunchKernelGGL((k_kv_attn_join<HD, true>), g, dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((k_kv_attn_join<HD, false>), g, dim3(256), 0, st, p);
 }
 
 }  // namespace
@@ -1044,7 +1055,7 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
   if (plan.own.slots) {
     Attn x = p;
     x.table = a.block_table, x.table_width = a.table_width, x.max_len = (int)a.max_kv;
-    x.causal = a.causal, x.target = plan.own.target;
+    x.causal = a.causal, x.target = plan.own.target, x.joined = plan.prefix.slots > 0;
     x.slots = plan.own.slots, x.row_tiles = plan.own.row_tiles;
     x.opart = own, x.ml = ml_own, x.where = where;
     const unsigned g = (unsigned)part_grid(a, plan.own);
@@ -1058,10 +1069,9 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
     x.tokens = p.tokens, x.heads = p.heads, x.kv_heads = p.kv_heads, x.group = p.group, x.hd = p.hd;
     x.max_q = p.max_q, x.n_prefix = plan.prefix.slots;
     x.where = plan.own.target > 0.0f ? where : nullptr;
-    const dim3 g((unsigned)(a.max_q * a.heads), (unsigned)a.batch);
-    if (p.hd <= 64) launch_join<64>(x, f32, g, st);
-    else if (p.hd <= 128) launch_join<128>(x, f32, g, st);
-    else launch_join<256>(x, f32, g, st);
+    if (p.hd <= 64) launch_join<64>(x, a, plan, st);
+    else if (p.hd <= 128) launch_join<128>(x, a, plan, st);
+    else launch_join<256>(x, a, plan, st);
   }
   return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
