@@ -144,11 +144,13 @@ struct Share {
 };
 
 __device__ __forceinline__ bool share_of(const Attn &p, int lane, Share &s) {
+  // slots last: those without a piece come at the end, and the pieces, which are dealt to the
+  // chip's eight dies in turn, fall on all of them
   int w = blockIdx.x;
-  const int slot = w % p.slots;
-  w /= p.slots;
   s.h = w % p.kv_heads;
-  s.rt = p.row_tiles - 1 - w / p.kv_heads;  // the tiles that see most tokens first
+  w /= p.kv_heads;
+  s.rt = p.row_tiles - 1 - w % p.row_tiles;  // the tiles that see most tokens first
+  const int slot = w / p.row_tiles;
   s.direct = p.direct;
   if (p.prefix || p.target == 0.0f) {
     s.j = job_of(p, p.prefix ? 0 : slot);
