@@ -26,30 +26,44 @@ typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 typedef float f2 __attribute__((ext_vector_type(2)));
+typedef unsigned u2 __attribute__((ext_vector_type(2)));
+typedef unsigned u4 __attribute__((ext_vector_type(4)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
+#ifndef ROWS_OCC
+#define ROWS_OCC 4
+#endif
 constexpr float kLn2 = 0.6931471805599453f;
+
+// A token list and the query rows that read it: the shared prefix (all rows of the call over one
+// page list), or the sequences' own tokens.
+struct List {
+  const int32_t *table;
+  int64_t table_width;
+  int max_len, causal, prefix;
+  int row_tiles, slots;
+  float target;  // own tokens: pieces wanted in all; 0 for one piece a sequence
+  int piece;     // prefix: tokens of a piece
+  int joined;    // own tokens: their rows have prefix pieces too
+  float *opart;
+  float2 *ml;
+  int2 *where;   // own tokens: first slot and pieces of a sequence that has any
+};
 
 struct Attn {
   const uint8_t *kc, *ks, *vc, *vs;
   const float *S_k, *S_v;
   const void *q;
   int64_t q_ts, q_hs;
-  const int32_t *q_offsets, *table, *kv_lens;
-  int64_t table_width;
-  int tokens, heads, kv_heads, group, hd, page_shift, pages, max_q, max_len, causal;
+  const int32_t *q_offsets, *kv_lens;
+  int tokens, heads, kv_heads, group, hd, page_shift, pages, max_q, batch;
   float scale;
-  int prefix;    // the job is the shared prefix: all tokens over one page list
-  int batch, row_tiles, slots;
-  float target;  // own tokens: pieces wanted in all; 0 for one piece a sequence
-  int piece;     // prefix: tokens of a piece
   int direct;    // one piece a row, written straight to out
-  int joined;    // rows have prefix pieces too
+  int first;     // workgroups of list[0]; the others are list[1]'s
   void *out;
-  float *lse, *opart;
-  float2 *ml;
-  int2 *where;   // first slot and pieces of a sequence that has any
+  float *lse;
+  List list[2];
 };
 
 // One sequence's share of the call.
@@ -58,10 +72,10 @@ struct Job {
   const int32_t *pages;
 };
 
-__device__ __forceinline__ Job job_of(const Attn &p, int b) {
+__device__ __forceinline__ Job job_of(const Attn &p, const List &k, int b) {
   Job j;
-  if (p.prefix) {
-    j.q0 = 0, j.nq = p.tokens, j.len = p.max_len, j.causal = 0, j.pages = p.table;
+  if (k.prefix) {
+    j.q0 = 0, j.nq = p.tokens, j.len = k.max_len, j.causal = 0, j.pages = k.table;
   } else {
     int lo = b * p.max_q, hi = lo + p.max_q;
     if (p.q_offsets) {
@@ -69,9 +83,9 @@ __device__ __forceinline__ Job job_of(const Attn &p, int b) {
       hi = min(max(p.q_offsets[b + 1], lo), min(p.tokens, lo + p.max_q));
     }
     j.q0 = lo, j.nq = hi - lo;
-    j.len = p.kv_lens ? min(max(p.kv_lens[b], 0), p.max_len) : 0;
-    j.causal = p.causal;
-    j.pages = p.table + b * p.table_width;
+    j.len = p.kv_lens ? min(max(p.kv_lens[b], 0), k.max_len) : 0;
+    j.causal = k.causal;
+    j.pages = k.table + b * k.table_width;
   }
   return j;
 }
@@ -136,38 +150,45 @@ __device__ __forceinline__ Piece find_piece(const int32_t *kv_lens, int batch, i
 }
 
 // A workgroup's share of the call: a row tile of one key/value head, tokens t0 .. t1 - 1, and
-// where its rows go: row r of the job to partial row `part + r` unless direct.
+// its list and slot (where its partial rows go, unless direct).
 struct Share {
   Job j;
-  int h, rt, t0, t1, direct;
-  int64_t part;
+  int h, rt, t0, t1, direct, list, slot;
 };
+
+// the first partial row of the job
+__device__ __forceinline__ int64_t part_of(const Attn &p, const Share &s) {
+  const int rows = p.list[s.list].prefix ? p.tokens * p.group : p.max_q * p.group;
+  return ((int64_t)s.slot * p.kv_heads + s.h) * rows;
+}
 
 __device__ __forceinline__ bool share_of(const Attn &p, int lane, Share &s) {
   // slots last: those without a piece come at the end, and the pieces, which are dealt to the
   // chip's eight dies in turn, fall on all of them
   int w = blockIdx.x;
+  const int second = w >= p.first;
+  if (second) w -= p.first;
+  const List &k = p.list[second];
   s.h = w % p.kv_heads;
   w /= p.kv_heads;
-  s.rt = p.row_tiles - 1 - w % p.row_tiles;  // the tiles that see most tokens first
-  const int slot = w / p.row_tiles;
+  s.rt = k.row_tiles - 1 - w % k.row_tiles;  // the tiles that see most tokens first
+  const int slot = w / k.row_tiles;
   s.direct = p.direct;
-  if (p.prefix || p.target == 0.0f) {
-    s.j = job_of(p, p.prefix ? 0 : slot);
-    s.t0 = p.prefix ? slot * p.piece : 0;
-    s.t1 = p.prefix ? min(s.j.len, s.t0 + p.piece) : s.j.len;
+  if (k.prefix || k.target == 0.0f) {
+    s.j = job_of(p, k, k.prefix ? 0 : slot);
+    s.t0 = k.prefix ? slot * k.piece : 0;
+    s.t1 = k.prefix ? min(s.j.len, s.t0 + k.piece) : s.j.len;
   } else {
-    const Piece x = find_piece(p.kv_lens, p.batch, p.max_len, p.target, slot, lane);
+    const Piece x = find_piece(p.kv_lens, p.batch, k.max_len, k.target, slot, lane);
     if (x.b < 0) return false;
-    s.direct = x.count == 1 && !p.joined;  // the join skips such sequences
+    s.direct = x.count == 1 && !k.joined;  // the join skips such sequences
     if (slot == x.first && s.h == 0 && s.rt == 0 && threadIdx.x == 0)
-      p.where[x.b] = make_int2(x.first, x.count);  // for the join
-    s.j = job_of(p, x.b);
+      k.where[x.b] = make_int2(x.first, x.count);  // for the join
+    s.j = job_of(p, k, x.b);
     s.t0 = (slot - x.first) * x.tokens;
     s.t1 = min(s.j.len, s.t0 + x.tokens);
   }
-  const int rows = p.prefix ? p.tokens * p.group : p.max_q * p.group;
-  s.part = ((int64_t)slot * p.kv_heads + s.h) * rows;
+  s.list = second, s.slot = slot;
   return true;
 }
 
@@ -202,94 +223,117 @@ constexpr int more(int a) { return a > 1 ? a : 1; }
 template <int HD>
 struct Group {
   unsigned k[HD / 32];             // HD/4 key codes of token i, from channel quad HD/4
-  unsigned ks;                     // their HD/64 scale bytes
+  unsigned ks;                     // a word of scales with theirs in it (scale_bits)
   unsigned v[4][more(HD / 128)];   // HD/16 value codes of tokens 4 quad + 0..3, from channel i HD/16
-  unsigned vs;                     // HD/64 value scale bytes of token lane / 4
+  unsigned vs;                     // the same for HD/64 value scales of token lane / 4
 };
 
-// Page ids of a token range, read ahead: lane k holds the id of the k-th group of a run of 1024
-// tokens, so a group takes its id from a register and no load waits for another.
+// Scales are loaded as whole words, so that nothing is done to them before they are used (a
+// narrow load's zero extension would wait for it at once). Part q of a token's four: the
+// lane's HD/64 bytes, moved down.
+template <int HD, bool EXACT>
+__device__ __forceinline__ unsigned scale_bits(unsigned w, unsigned q) {
+  if (!EXACT || HD > 128) return w;
+  return HD == 128 ? w >> 16 * (q & 1) : w >> 8 * q;
+}
+
+// Page ids of a token range: lane k of `ids` holds the id of the k-th group of 16 tokens of the
+// run of 1024 at t, `next` those of the run after it, so a group takes its id from a register
+// and its loads wait for nothing. A run is left (`advance`) outside the loop over its tiles:
+// a conditional load inside it would have every iteration wait for its own new loads.
+constexpr int kRun = 1024;
+
 struct Pages {
-  int t0, run;    // the range's first token; the run in ids
-  int ids, next;  // this run's, the next one's
+  int t, ids, next;
 };
 
-__device__ __forceinline__ int load_ids(const Attn &p, const Job &j, int t, int t_end, int lane) {
+__device__ __forceinline__ int load_ids(const Job &j, int page_shift, int t, int t_end, int lane) {
   t += 16 * lane;
-  return t < t_end ? j.pages[t >> p.page_shift] : -1;
+  return t < t_end ? j.pages[t >> page_shift] : -1;
 }
 
-__device__ __forceinline__ Pages open_pages(const Attn &p, const Job &j, int t0, int t_end, int lane) {
-  return {t0, 0, load_ids(p, j, t0, t_end, lane), load_ids(p, j, t0 + 1024, t_end, lane)};
+__device__ __forceinline__ Pages open_pages(const Job &j, int page_shift, int t0, int t_end, int lane) {
+  return {t0, load_ids(j, page_shift, t0, t_end, lane), load_ids(j, page_shift, t0 + kRun, t_end, lane)};
 }
 
-// The page of the group at t; runs are asked for in ascending order.
-__device__ __forceinline__ int page_of(const Attn &p, const Job &j, Pages &pg, int t, int t_end, int lane) {
-  const int run = (t - pg.t0) >> 10;
-  if (run != pg.run) {
-    pg.run = run;
-    pg.ids = pg.next;
-    pg.next = load_ids(p, j, pg.t0 + 1024 * (run + 1), t_end, lane);
-  }
-  return __builtin_amdgcn_readlane(pg.ids, (t - pg.t0) >> 4 & 63);
+__device__ __forceinline__ void advance(Pages &pg, const Job &j, int page_shift, int t_end, int lane) {
+  pg.t += kRun;
+  pg.ids = pg.next;
+  pg.next = load_ids(j, page_shift, pg.t + kRun, t_end, lane);
+}
+
+__device__ __forceinline__ int page_of(const Pages &pg, int t) {
+  const int g = (t - pg.t) >> 4;
+  if (g < kRun / 16) return __builtin_amdgcn_readlane(pg.ids, g);
+  return __builtin_amdgcn_readlane(pg.next, g - kRun / 16);
 }
 
 // Loads the group at t of page `id`; returns whether the page is one of the cache's. A group
 // that is not there is read from page 0 and never used.
+#define GLOBAL __attribute__((address_space(1)))
+
+// An unsigned lane offset that stays 32 bits beside a scalar base address (hoisted out of a loop
+// as 64 bits it would take two registers, and every load a 64-bit addition).
+__device__ __forceinline__ unsigned lane_offset(unsigned o) {
+  asm volatile("" : "+v"(o));
+  return o;
+}
+
 template <int HD, bool EXACT>
 __device__ __forceinline__ int load_group(const Attn &p, int id, int h, int t, int lane, Group<HD> &x) {
-  const int i = lane & 15, quad = lane >> 4;
-  const int nb = EXACT ? HD / 16 : p.hd >> 4;  // blocks of a row
+  // uniform base addresses and unsigned lane offsets
+  const unsigned i = lane & 15, quad = lane >> 4, l = lane;
+  const unsigned nb = EXACT ? HD / 16 : (unsigned)p.hd >> 4;  // blocks of a row
   const int ok = id >= 0 && id < p.pages;
   const int64_t row = (((int64_t)(ok ? id : 0) * p.kv_heads + h) << p.page_shift) +
                       (t & ((1 << p.page_shift) - 1));
-  const uint8_t *kc = p.kc + row * (nb * 8), *ks = p.ks + row * nb;
-  const uint8_t *vc = p.vc + row * (nb * 8), *vs = p.vs + row * nb;
+  typedef const GLOBAL uint8_t *Bytes;
+  Bytes kc = (Bytes)(p.kc + row * (nb * 8)), ks = (Bytes)(p.ks + row * nb);
+  Bytes vc = (Bytes)(p.vc + row * (nb * 8)), vs = (Bytes)(p.vs + row * nb);
   if (EXACT) {
-    const unsigned *k = reinterpret_cast<const unsigned *>(kc + i * (nb * 8) + quad * (HD / 8));
+    const unsigned ko = lane_offset(i * (nb * 8) + quad * (HD / 8));
     if constexpr (HD == 64) {
-      const uint2 a = *reinterpret_cast<const uint2 *>(k);
+      const u2 a = *(const GLOBAL u2 *)(kc + ko);
       x.k[0] = a.x, x.k[1] = a.y;
     } else {
 #pragma unroll
       for (int w = 0; w < HD / 128; ++w) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(k + 4 * w);
+        const u4 a = *(const GLOBAL u4 *)(kc + ko + 16 * w);
         x.k[4 * w] = a.x, x.k[4 * w + 1] = a.y, x.k[4 * w + 2] = a.z, x.k[4 * w + 3] = a.w;
       }
     }
-    ks += i * nb + quad * (HD / 64), vs += (lane >> 2) * nb + (lane & 3) * (HD / 64);
-    if constexpr (HD == 64) {
-      x.ks = *ks, x.vs = *vs;
-    } else if constexpr (HD == 128) {
-      x.ks = *reinterpret_cast<const uint16_t *>(ks), x.vs = *reinterpret_cast<const uint16_t *>(vs);
-    } else {
-      x.ks = *reinterpret_cast<const unsigned *>(ks), x.vs = *reinterpret_cast<const unsigned *>(vs);
-    }
+    const unsigned kq = HD == 64 ? 0 : HD == 128 ? quad & 2 : quad * 4;
+    const unsigned vq = HD == 64 ? 0 : HD == 128 ? l & 2 : (l & 3) * 4;
+    const unsigned kso = lane_offset(i * nb + (HD == 128 ? kq * 2 : kq));
+    const unsigned vso = lane_offset((l >> 2) * nb + (HD == 128 ? vq * 2 : vq));
+    x.ks = *(const GLOBAL unsigned *)(ks + kso);
+    x.vs = *(const GLOBAL unsigned *)(vs + vso);
   } else {
     x.ks = x.vs = 0;
 #pragma unroll
-    for (int w = 0; w < HD / 64; ++w) {
-      const int b = quad * (HD / 64) + w, c = (lane & 3) * (HD / 64) + w;
-      uint2 a = make_uint2(0, 0);
+    for (unsigned w = 0; w < HD / 64; ++w) {
+      const unsigned b = quad * (HD / 64) + w, c = (l & 3) * (HD / 64) + w;
+      u2 a = (u2){0, 0};
       if (b < nb) {
-        a = *reinterpret_cast<const uint2 *>(kc + (i * nb + b) * 8);
+        a = *(const GLOBAL u2 *)(kc + (i * nb + b) * 8);
         x.ks |= (unsigned)ks[i * nb + b] << (8 * w);
       }
       x.k[2 * w] = a.x, x.k[2 * w + 1] = a.y;
-      if (c < nb) x.vs |= (unsigned)vs[(lane >> 2) * nb + c] << (8 * w);
+      if (c < nb) x.vs |= (unsigned)vs[(l >> 2) * nb + c] << (8 * w);
     }
   }
-  const bool in = EXACT || i * (HD / 16) < p.hd;
+  const bool in = EXACT || (int)(i * (HD / 16)) < p.hd;
+  const unsigned vo = lane_offset(4 * quad * (nb * 8) + i * (HD / 32));
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint8_t *v = vc + (4 * quad + e) * (nb * 8) + i * (HD / 32);
+  for (unsigned e = 0; e < 4; ++e) {
+    const Bytes v = vc + e * (nb * 8);
     x.v[e][0] = 0;
     if constexpr (HD > 128) x.v[e][1] = 0;
     if (in) {
-      if constexpr (HD == 64) x.v[e][0] = *reinterpret_cast<const uint16_t *>(v);
-      else if constexpr (HD == 128) x.v[e][0] = *reinterpret_cast<const unsigned *>(v);
+      if constexpr (HD == 64) x.v[e][0] = *(const GLOBAL uint16_t *)(v + vo);
+      else if constexpr (HD == 128) x.v[e][0] = *(const GLOBAL unsigned *)(v + vo);
       else {
-        const uint2 a = *reinterpret_cast<const uint2 *>(v);
+        const u2 a = *(const GLOBAL u2 *)(v + vo);
         x.v[e][0] = a.x, x.v[e][1] = a.y;
       }
     }
@@ -298,11 +342,11 @@ __device__ __forceinline__ int load_group(const Attn &p, int id, int h, int t, i
 }
 
 // Key operands of a group: out[s] holds eight channels of the lane's token, contraction step s.
-template <int HD>
-__device__ __forceinline__ void key_frags(const Group<HD> &x, h8 *out) {
+template <int HD, bool EXACT>
+__device__ __forceinline__ void key_frags(const Group<HD> &x, int lane, h8 *out) {
   h2 sc[more(HD / 128)];
 #pragma unroll
-  for (int k = 0; k < more(HD / 128); ++k) sc[k] = scales2(x.ks, k);
+  for (int k = 0; k < more(HD / 128); ++k) sc[k] = scales2(scale_bits<HD, EXACT>(x.ks, lane >> 4), k);
 #pragma unroll
   for (int s = 0; s < HD / 32; ++s) {
     const _Float16 f = (s >> 1) & 1 ? sc[s >> 2][1] : sc[s >> 2][0];
@@ -318,12 +362,12 @@ __device__ __forceinline__ void key_frags(const Group<HD> &x, h8 *out) {
 // that the eight-byte reads of a half wave fall on different banks.
 constexpr int kVsRow = 20;
 
-template <int HD>
+template <int HD, bool EXACT>
 __device__ __forceinline__ void stage_value_scales(const Group<HD> &x, int lane, _Float16 *lds) {
   const int tok = lane >> 2, b0 = (lane & 3) * (HD / 64);
 #pragma unroll
   for (int w = 0; w < more(HD / 128); ++w) {
-    const h2 s = scales2(x.vs, w);
+    const h2 s = scales2(scale_bits<HD, EXACT>(x.vs, lane & 3), w);
     lds[(b0 + 2 * w) * kVsRow + tok] = s[0];
     if (HD > 64) lds[(b0 + 2 * w + 1) * kVsRow + tok] = s[1];
   }
@@ -336,28 +380,38 @@ __device__ __forceinline__ void order_wave_lds() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
-// Value operands of a group: out[c] holds channel i HD/16 + c of the lane's four tokens. The
-// codes of two tokens are interleaved nibble by nibble first, so that one convert gives a
-// pair of tokens of one channel.
+// Scales of the lane's four value tokens, in pairs.
+template <int HD>
+__device__ __forceinline__ void value_scales(int lane, const _Float16 *lds, h2 *sc) {
+  const h4 s = *reinterpret_cast<const h4 *>(lds + (((lane & 15) * (HD / 16)) >> 4) * kVsRow + 4 * (lane >> 4));
+  sc[0] = (h2){s[0], s[1]}, sc[1] = (h2){s[2], s[3]};
+}
+
+// The codes of token pair e (0 or 1), interleaved nibble by nibble: byte b of `even` holds
+// channel 2 b of both tokens, of `odd` channel 2 b + 1, so that one convert gives a pair.
+template <int HD>
+__device__ __forceinline__ void value_nibbles(const Group<HD> &x, int e, int word, unsigned &even,
+                                              unsigned &odd) {
+  const unsigned a = x.v[2 * e][word], b = x.v[2 * e + 1][word];
+  even = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+  odd = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+}
+
+// Value operands of a group: out[c] holds channel i HD/16 + c of the lane's four tokens.
 template <int HD>
 __device__ __forceinline__ void value_frags(const Group<HD> &x, int lane, const _Float16 *lds, h4 *out) {
-  const int i = lane & 15, quad = lane >> 4;
-  const h4 s = *reinterpret_cast<const h4 *>(lds + ((i * (HD / 16)) >> 4) * kVsRow + 4 * quad);
-  const h2 sc[2] = {{s[0], s[1]}, {s[2], s[3]}};
+  h2 sc[2];
+  value_scales<HD>(lane, lds, sc);
   constexpr int C = HD >= 128 ? 8 : HD / 16;  // channels of a word
 #pragma unroll
   for (int word = 0; word < more(HD / 128); ++word) {
     union { h4 v; h2 p[2]; } r[C];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const unsigned a = x.v[2 * e][word], b = x.v[2 * e + 1][word];
-      const unsigned even = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
-      const unsigned odd = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+      unsigned even, odd;
+      value_nibbles(x, e, word, even, odd);
 #pragma unroll
-      for (int c = 0; c < C; c += 2) {
-        r[c].p[e] = codes2(even, c >> 1) * sc[e];
-        r[c + 1].p[e] = codes2(odd, c >> 1) * sc[e];
-      }
+      for (int c = 0; c < C; ++c) r[c].p[e] = codes2(c & 1 ? odd : even, c >> 1) * sc[e];
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) out[8 * word + c] = r[c].v;
@@ -524,7 +578,7 @@ __device__ __forceinline__ void probabilities(f4 (*s)[2], Rows<HD, NT, F32> &x, 
 // Four waves take the 32-token tiles of a piece in turn, each for the same 16 NT query rows,
 // and join their sums at the end.
 template <int HD, int NT, bool F32, bool EXACT>
-__global__ void __launch_bounds__(256, NT == 1 && HD <= 128 && !F32 ? 4 : 1) k_kv_attn_rows(Attn p) {
+__global__ void __launch_bounds__(256, NT == 1 && HD <= 128 && !F32 ? ROWS_OCC : 1) k_kv_attn_rows(Attn p) {
   constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, OROW = HD + 4;
   constexpr float kBase = base_of(F32);
   __shared__ __align__(16) float smem[4 * 16 * OROW];
@@ -540,34 +594,37 @@ __global__ void __launch_bounds__(256, NT == 1 && HD <= 128 && !F32 ? 4 : 1) k_k
   if (r0 >= rows) return;
   int t1 = sh.t1;
 
-  Rows<HD, NT, F32> x;
-  load_rows<HD, NT, F32, EXACT>(p, j, h, r0, rows, lane, x);
   int lim_lo, lim_hi;
   row_limits(p, j, r0, min(r0 + 16 * NT, rows), lim_lo, lim_hi);
   t1 = min(t1, lim_hi);
 
-  Group<HD> cur[2], nxt[2];
+  Group<HD> g[2], nxt[2];  // raw codes: this tile's, and the next one's on their way
   int ok = 0, nxt_ok = 0;
-  Pages pg = open_pages(p, j, t0, t1, lane);
+  Pages pg = open_pages(j, p.page_shift, t0, t1, lane);
+  Rows<HD, NT, F32> x;
+  load_rows<HD, NT, F32, EXACT>(p, j, h, r0, rows, lane, x);
   int t = t0 + 32 * wave;
-  if (t < t1)
+  if (t < t1) {
+#pragma unroll
     for (int u = 0; u < 2; ++u)
-      ok |= load_group<HD, EXACT>(p, page_of(p, j, pg, t + 16 * u, t1, lane), h, t + 16 * u, lane, cur[u]) << u;
-  for (; t < t1; t += 128) {
+      ok |= load_group<HD, EXACT>(p, page_of(pg, t + 16 * u), h, t + 16 * u, lane, g[u]) << u;
+  }
+  for (; t < t1; advance(pg, j, p.page_shift, t1, lane))
+  for (const int te = min(t1, pg.t + kRun); t < te; t += 128) {
     if (t + 128 < t1) {
       nxt_ok = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int tt = t + 128 + 16 * u;
-        nxt_ok |= load_group<HD, EXACT>(p, page_of(p, j, pg, tt, t1, lane), h, tt, lane, nxt[u]) << u;
+        nxt_ok |= load_group<HD, EXACT>(p, page_of(pg, tt), h, tt, lane, nxt[u]) << u;
       }
     }
     f4 s[NT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      stage_value_scales<HD>(cur[u], lane, vs_lds[wave][u]);
+      stage_value_scales<HD, EXACT>(g[u], lane, vs_lds[wave][u]);
       h8 kf[HD / 32];
-      key_frags<HD>(cur[u], kf);
+      key_frags<HD, EXACT>(g[u], lane, kf);
 #pragma unroll
       for (int n = 0; n < NT; ++n) s[n][u] = (f4){0, 0, 0, 0};
 #pragma unroll
@@ -577,30 +634,44 @@ __global__ void __launch_bounds__(256, NT == 1 && HD <= 128 && !F32 ? 4 : 1) k_k
 #pragma unroll
           for (int q = 0; q < HALVES; ++q)
             s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[k], x.q[n][q][k], s[n][u], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);  // one group's operands at a time: registers
     }
     order_wave_lds();
     if (t + 32 > lim_lo || ok != 3) hide<NT>(s, x.lim, t, t1, ok, quad);
     h8 pf[NT][HALVES];
     probabilities<HD, NT, F32>(s, x, pf);
-    h4 v0[DV], v1[DV];
-    value_frags<HD>(cur[0], lane, vs_lds[wave][0], v0);
-    value_frags<HD>(cur[1], lane, vs_lds[wave][1], v1);
+    __builtin_amdgcn_sched_barrier(0);
+    // as value_frags, two channels of all eight tokens at a time
+    h2 sc[2][2];
 #pragma unroll
-    for (int d = 0; d < DV; ++d) {
-      const h8 a = __builtin_shufflevector(v0[d], v1[d], 0, 1, 2, 3, 4, 5, 6, 7);
+    for (int u = 0; u < 2; ++u) value_scales<HD>(lane, vs_lds[wave][u], sc[u]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int word = 0; word < more(HD / 128); ++word) {
+      unsigned even[4], odd[4];
 #pragma unroll
-        for (int q = 0; q < HALVES; ++q)
-          x.acc[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf[n][q], x.acc[n][d], 0, 0, 0);
+      for (int e = 0; e < 4; ++e) value_nibbles(g[e >> 1], e & 1, word, even[e], odd[e]);
+#pragma unroll
+      for (int c = 0; c < (HD >= 128 ? 8 : HD / 16); ++c) {
+        union { h8 v; h2 p[4]; } a;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a.p[e] = codes2(c & 1 ? odd[e] : even[e], c >> 1) * sc[e >> 1][e & 1];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int q = 0; q < HALVES; ++q)
+            x.acc[n][8 * word + c] =
+                __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v, pf[n][q], x.acc[n][8 * word + c], 0, 0, 0);
+        if (c & 1) __builtin_amdgcn_sched_barrier(0);
+      }
     }
     order_wave_lds();
 #pragma unroll
-    for (int u = 0; u < 2; ++u) cur[u] = nxt[u];
+    for (int u = 0; u < 2; ++u) g[u] = nxt[u];
     ok = nxt_ok;
   }
 
   // join the four waves
+  const int64_t part = part_of(p, sh);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     x.l[n] += xor16(x.l[n]);
@@ -647,13 +718,13 @@ __global__ void __launch_bounds__(256, NT == 1 && HD <= 128 && !F32 ? 4 : 1) k_k
         if (sh.direct)
           store_out<F32>(p.out, at * p.hd + d, y.x * f, y.y * f);
         else
-          *reinterpret_cast<float2 *>(p.opart + (sh.part + r) * p.hd + d) = y;
+          *reinterpret_cast<float2 *>(p.list[sh.list].opart + (part + r) * p.hd + d) = y;
       }
       if ((threadIdx.x & 15) == 0) {
         if (sh.direct) {
           if (p.lse) p.lse[at] = ll > 0.0f ? kLn2 * (mm - kBase + __builtin_amdgcn_logf(ll)) : -INFINITY;
         } else {
-          p.ml[sh.part + r] = make_float2(mm - kBase, ll);
+          p.list[sh.list].ml[part + r] = make_float2(mm - kBase, ll);
         }
       }
     }
@@ -685,8 +756,6 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   int t1 = sh.t1;
   const int r0 = R0 + wave * 16 * NT;
 
-  Rows<HD, NT, F32> x;
-  load_rows<HD, NT, F32, EXACT>(p, j, h, r0, rows, lane, x);
   int lim_lo, lim_hi, none;
   row_limits(p, j, R0, min(R0 + 16 * NT * W, rows), none, lim_hi);
   t1 = min(t1, lim_hi);
@@ -695,16 +764,16 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
 
   Group<HD> g;
   int ok = 0;
-  Pages pg = open_pages(p, j, t0, t1, lane);
+  Pages pg = open_pages(j, p.page_shift, t0, t1, lane);
   const auto fetch = [&](int t) {  // this wave's group of the stage at t
     t += 16 * wave;
-    ok = load_group<HD, EXACT>(p, page_of(p, j, pg, t, t1, lane), h, t, lane, g);
+    ok = load_group<HD, EXACT>(p, page_of(pg, t), h, t, lane, g);
   };
   const auto dequantise = [&](int b) {
-    stage_value_scales<HD>(g, lane, vs_lds[wave]);
+    stage_value_scales<HD, EXACT>(g, lane, vs_lds[wave]);
     if (lane == 0) oks[b][wave] = ok;
     h8 kf[KS];
-    key_frags<HD>(g, kf);
+    key_frags<HD, EXACT>(g, lane, kf);
 #pragma unroll
     for (int k = 0; k < KS; ++k) kfrag[b][wave][k][lane] = kf[k];
     order_wave_lds();
@@ -715,14 +784,17 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
       reinterpret_cast<h4 *>(&vfrag[b][wave >> 1][d][lane])[wave & 1] = vf[d];
     order_wave_lds();
   };
+  if (t0 < t1) fetch(t0);
+  Rows<HD, NT, F32> x;
+  load_rows<HD, NT, F32, EXACT>(p, j, h, r0, rows, lane, x);
   if (t0 < t1) {
-    fetch(t0);
     dequantise(0);
     if (t0 + STAGE < t1) fetch(t0 + STAGE);
   }
   __syncthreads();
-  int b = 0;
-  for (int t = t0; t < t1; t += STAGE, b ^= 1) {
+  int b = 0, t = t0;
+  for (; t < t1; advance(pg, j, p.page_shift, t1, lane))
+  for (const int te = min(t1, pg.t + kRun); t < te; t += STAGE, b ^= 1) {
     // operands are read one step ahead of their products: the values' before the exponentials,
     // the next tile's keys before the second product
     const int tiles = min(W / 2, (min(t1, lim_hi) - t + 31) >> 5);
@@ -774,6 +846,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   }
 
   // each lane holds HD/16 consecutive channels of its row four times
+  const int64_t part = part_of(p, sh);
   const float S_v = p.S_v[h];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -795,7 +868,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
           if (sh.direct)
             store_out<F32>(p.out, at * p.hd + ch + d, a, b);
           else
-            *reinterpret_cast<float2 *>(p.opart + (sh.part + r) * p.hd + ch + d) = make_float2(a, b);
+            *reinterpret_cast<float2 *>(p.list[sh.list].opart + (part + r) * p.hd + ch + d) = make_float2(a, b);
         }
       }
     }
@@ -803,7 +876,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
       if (sh.direct) {
         if (p.lse) p.lse[at] = l > 0.0f ? kLn2 * (__builtin_amdgcn_logf(l) - x.off[n]) : -INFINITY;
       } else {
-        p.ml[sh.part + r] = make_float2(-x.off[n], l);
+        p.list[sh.list].ml[part + r] = make_float2(-x.off[n], l);
       }
     }
   }
@@ -911,41 +984,59 @@ struct Plan {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Up to 32 rows a (sequence, key/value head): k_kv_attn_rows, whose waves work alone; more:
-// k_kv_attn_tile, whose waves share what they dequantise. Workgroups a CU holds: by registers
-// (HD and NT) for the first, by LDS (1 KiB a token at HD 256, two stages) for the second.
-Part plan_rows(const KvAttention &a, int64_t rows) {
+// k_kv_attn_rows with 16 NT rows a workgroup; workgroups a CU holds, by registers.
+Part rows_part(const KvAttention &a, int64_t rows, int nt) {
+  Part r = {};
+  const bool wide = a.cache->head_dim > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
+  const int one = wide ? (f32 ? 1 : 2) : (f32 ? 3 : ROWS_OCC);
+  r.nt = nt;
+  r.resident = 256 * (nt == 1 ? one : (one + 1) / 2);
+  r.row_tiles = (int)cdiv(rows, 16 * nt);
+  return r;
+}
+
+// k_kv_attn_tile: workgroups a CU holds, by LDS (at HD 256 1 KiB a token, two stages).
+Part tile_part(const KvAttention &a, int64_t rows) {
   Part r = {};
   const int64_t hd = a.cache->head_dim;
   const bool wide = hd > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
-  int per_cu;
-  if (rows > 32) {
-    r.nt = wide || f32 || rows <= 64 ? 1 : 2;
-    r.waves = wide || rows <= 64 * r.nt ? 4 : 8;
-    per_cu = wide ? 1 : (hd > 64 || r.waves == 8 ? 8 / r.waves : 3);
-  } else {
-    r.nt = rows <= 16 ? 1 : 2;
-    const int one = wide ? (f32 ? 1 : 2) : (f32 ? 3 : 4);
-    per_cu = r.nt == 1 || one == 1 ? one : one / 2;
-  }
-  r.resident = 256 * per_cu;
-  r.row_tiles = (int)cdiv(rows, 16 * r.nt * (r.waves ? r.waves : 1));
+  r.nt = wide || f32 || rows <= 64 ? 1 : 2;
+  r.waves = wide || rows <= 64 * r.nt ? 4 : 8;
+  r.resident = 256 * (wide ? 1 : (hd > 64 || r.waves == 8 ? 8 / r.waves : 3));
+  r.row_tiles = (int)cdiv(rows, 16 * r.nt * r.waves);
   return r;
+}
+
+// Rows a (sequence, key/value head): up to 32 to k_kv_attn_rows, whose waves work alone; more to
+// k_kv_attn_tile, whose waves share what they dequantise.
+Part plan_rows(const KvAttention &a, int64_t rows) {
+  if (rows > 32) return tile_part(a, rows);
+  const bool one = rows <= 16 || (a.cache->head_dim > 128 && a.dtype == NVFP4_DTYPE_F32);
+  return rows_part(a, rows, one ? 1 : 2);
 }
 
 Plan plan_of(const KvAttention &a) {
   Plan p = {};
-  const int64_t G = a.heads / a.cache->kv_heads;
+  const int64_t G = a.heads / a.cache->kv_heads, kvh = a.cache->kv_heads;
+  const bool own = a.max_kv > 0 || a.prefix_len == 0;
+  if (own) p.own = plan_rows(a, a.max_q * G);
   if (a.prefix_len > 0) {
-    Part &r = p.prefix = plan_rows(a, a.tokens * G);
-    const int64_t units = a.cache->kv_heads * r.row_tiles;
+    p.prefix = plan_rows(a, a.tokens * G);
+    // one launch for both lists where the prefix is so short that the own tokens' kernel does it
+    // in one round of 128-token pieces
+    if (own && !p.own.waves) {
+      const Part r = rows_part(a, a.tokens * G, p.own.nt);
+      if (r.row_tiles * kvh * cdiv(a.prefix_len, 128) <= r.resident) p.prefix = r;
+    }
+    Part &r = p.prefix;
+    const int64_t units = kvh * r.row_tiles;
     const int64_t n = units < r.resident ? r.resident / units : 1;
     r.piece = (int)(cdiv(a.prefix_len, 128 * n) * 128);
     r.slots = (int)cdiv(a.prefix_len, r.piece);
   }
-  if (a.max_kv > 0 || a.prefix_len == 0) {
-    Part &r = p.own = plan_rows(a, a.max_q * G);
-    const int64_t units = a.cache->kv_heads * r.row_tiles;
+  if (own) {
+    Part &r = p.own;
+    const int64_t units = kvh * r.row_tiles;
     const int64_t most = a.batch * cdiv(a.max_kv, 128);  // pieces of 128 tokens
     const float target = (float)r.resident / (float)units;
     r.slots = (int)a.batch;
@@ -1045,25 +1136,28 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
   float2 *ml = reinterpret_cast<float2 *>(own + n_own * c.head_dim), *ml_own = ml + n_pre;
   int2 *where = reinterpret_cast<int2 *>(ml_own + n_own);
   const bool f32 = a.dtype == NVFP4_DTYPE_F32;
-  if (plan.prefix.slots) {
-    Attn x = p;
-    x.prefix = 1, x.table = a.prefix_pages, x.max_len = (int)a.prefix_len;
-    x.piece = plan.prefix.piece, x.slots = plan.prefix.slots, x.row_tiles = plan.prefix.row_tiles;
-    x.opart = opart, x.ml = ml;
-    const unsigned g = (unsigned)part_grid(a, plan.prefix);
-    if (f32) launch_hd<true>(x, plan.prefix, g, st);
-    else launch_hd<false>(x, plan.prefix, g, st);
-  }
-  if (plan.own.slots) {
-    Attn x = p;
-    x.table = a.block_table, x.table_width = a.table_width, x.max_len = (int)a.max_kv;
-    x.causal = a.causal, x.target = plan.own.target, x.joined = plan.prefix.slots > 0;
-    x.slots = plan.own.slots, x.row_tiles = plan.own.row_tiles;
-    x.opart = own, x.ml = ml_own, x.where = where;
-    const unsigned g = (unsigned)part_grid(a, plan.own);
-    if (f32) launch_hd<true>(x, plan.own, g, st);
-    else launch_hd<false>(x, plan.own, g, st);
-  }
+  List lists[2] = {};
+  const Part parts[2] = {plan.prefix, plan.own};
+  const int64_t grids[2] = {part_grid(a, plan.prefix), part_grid(a, plan.own)};
+  List &x = lists[0], &y = lists[1];
+  x.table = a.prefix_pages, x.max_len = (int)a.prefix_len, x.prefix = 1;
+  x.piece = plan.prefix.piece, x.opart = opart, x.ml = ml;
+  y.table = a.block_table, y.table_width = a.table_width, y.max_len = (int)a.max_kv;
+  y.causal = a.causal, y.target = plan.own.target, y.joined = plan.prefix.slots > 0;
+  y.opart = own, y.ml = ml_own, y.where = where;
+  for (int k = 0; k < 2; ++k)
+    lists[k].row_tiles = parts[k].row_tiles, lists[k].slots = parts[k].slots;
+  const auto launch = [&](int k, bool both) {
+    p.list[0] = lists[k], p.list[1] = lists[1];
+    p.first = (int)grids[k];
+    const unsigned g = (unsigned)(grids[k] + (both ? grids[1] : 0));
+    if (f32) launch_hd<true>(p, parts[k], g, st);
+    else launch_hd<false>(p, parts[k], g, st);
+  };
+  const bool both = grids[0] && grids[1] && parts[0].nt == parts[1].nt &&
+                    parts[0].waves == parts[1].waves && grids[0] + grids[1] <= INT32_MAX;
+  if (grids[0]) launch(0, both);
+  if (grids[1] && !both) launch(1, false);
   if (!plan.direct) {
     Join x = {};
     x.opart = opart, x.opart_own = own, x.ml = ml, x.ml_own = ml_own;
