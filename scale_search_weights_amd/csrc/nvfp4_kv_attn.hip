@@ -31,9 +31,6 @@ typedef unsigned u4 __attribute__((ext_vector_type(4)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
-#ifndef ROWS_OCC
-#define ROWS_OCC 4
-#endif
 constexpr float kLn2 = 0.6931471805599453f;
 
 // A token list and the query rows that read it: the shared prefix (all rows of the call over one
@@ -575,15 +572,15 @@ __device__ __forceinline__ void probabilities(f4 (*s)[2], Rows<HD, NT, F32> &x, 
   for (int n = 0; n < NT; ++n) x.l[n] += sum[n];
 }
 
-// Four waves take the 32-token tiles of a piece in turn, each for the same 16 NT query rows,
-// and join their sums at the end.
-template <int HD, int NT, bool F32, bool EXACT>
-__global__ void __launch_bounds__(256, NT == 1 && HD <= 128 && !F32 ? ROWS_OCC : 1) k_kv_attn_rows(Attn p) {
+// W waves take the 32-token tiles of a piece in turn, each for the same 16 NT query rows, and
+// join their sums at the end.
+template <int HD, int NT, bool F32, bool EXACT, int W>
+__global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) k_kv_attn_rows(Attn p) {
   constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, OROW = HD + 4;
   constexpr float kBase = base_of(F32);
-  __shared__ __align__(16) float smem[4 * 16 * OROW];
-  __shared__ __align__(16) _Float16 vs_lds[4][2][DV * kVsRow];
-  __shared__ float sm_m[4][16 * NT], sm_l[4][16 * NT];
+  __shared__ __align__(16) float smem[W * 16 * OROW];
+  __shared__ __align__(16) _Float16 vs_lds[W][2][DV * kVsRow];
+  __shared__ float sm_m[W][16 * NT], sm_l[W][16 * NT];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int i = lane & 15, quad = lane >> 4;
@@ -610,12 +607,12 @@ __global__ void __launch_bounds__(256, NT == 1 && HD <= 128 && !F32 ? ROWS_OCC :
       ok |= load_group<HD, EXACT>(p, page_of(pg, t + 16 * u), h, t + 16 * u, lane, g[u]) << u;
   }
   for (; t < t1; advance(pg, j, p.page_shift, t1, lane))
-  for (const int te = min(t1, pg.t + kRun); t < te; t += 128) {
-    if (t + 128 < t1) {
+  for (const int te = min(t1, pg.t + kRun); t < te; t += 32 * W) {
+    if (t + 32 * W < t1) {
       nxt_ok = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int tt = t + 128 + 16 * u;
+        const int tt = t + 32 * W + 16 * u;
         nxt_ok |= load_group<HD, EXACT>(p, page_of(pg, tt), h, tt, lane, nxt[u]) << u;
       }
     }
@@ -670,7 +667,7 @@ __global__ void __launch_bounds__(256, NT == 1 && HD <= 128 && !F32 ? ROWS_OCC :
     ok = nxt_ok;
   }
 
-  // join the four waves
+  // join the waves
   const int64_t part = part_of(p, sh);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -684,7 +681,7 @@ __global__ void __launch_bounds__(256, NT == 1 && HD <= 128 && !F32 ? ROWS_OCC :
   for (int n = 0; n < NT; ++n) {
     float M = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) M = fmaxf(M, sm_m[k][16 * n + i]);
+    for (int k = 0; k < W; ++k) M = fmaxf(M, sm_m[k][16 * n + i]);
     const float m = kBase - x.off[n];
     const float a = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
     if (n) __syncthreads();
@@ -694,24 +691,24 @@ __global__ void __launch_bounds__(256, NT == 1 && HD <= 128 && !F32 ? ROWS_OCC :
 #pragma unroll
       for (int d = 0; d < DV; ++d) o[DV * (4 * quad + r) + d] = x.acc[n][d][r] * a;
     __syncthreads();
-    // sixteen lanes a row, pairs of channels
-    const int row = threadIdx.x >> 4, r = r0 + 16 * n + row;
+    // 4 W lanes a row, pairs of channels
+    const int row = threadIdx.x / (4 * W), col = threadIdx.x % (4 * W), r = r0 + 16 * n + row;
     if (r < rows) {
       float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mm = fmaxf(mm, sm_m[k][16 * n + row]);
+      for (int k = 0; k < W; ++k) mm = fmaxf(mm, sm_m[k][16 * n + row]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < W; ++k) {
         const float mk = sm_m[k][16 * n + row];
         if (mk != -INFINITY) ll += sm_l[k][16 * n + row] * __builtin_amdgcn_exp2f(mk - mm);
       }
       const int tok = r / p.group, head = h * p.group + (r - tok * p.group);
       const int64_t at = (int64_t)(j.q0 + tok) * p.heads + head;
       const float f = sh.direct ? (ll > 0.0f ? S_v / ll : 0.0f) : 1.0f;
-      for (int d = 2 * (threadIdx.x & 15); d < p.hd; d += 32) {
+      for (int d = 2 * col; d < p.hd; d += 8 * W) {
         float2 y = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < W; ++k) {
           const f2 z = *reinterpret_cast<const f2 *>(smem + (k * 16 + row) * OROW + d);
           y.x += z[0], y.y += z[1];
         }
@@ -720,7 +717,7 @@ __global__ void __launch_bounds__(256, NT == 1 && HD <= 128 && !F32 ? ROWS_OCC :
         else
           *reinterpret_cast<float2 *>(p.list[sh.list].opart + (part + r) * p.hd + d) = y;
       }
-      if ((threadIdx.x & 15) == 0) {
+      if (col == 0) {
         if (sh.direct) {
           if (p.lse) p.lse[at] = ll > 0.0f ? kLn2 * (mm - kBase + __builtin_amdgcn_logf(ll)) : -INFINITY;
         } else {
@@ -971,7 +968,8 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
 namespace {
 
 struct Part {      // one launch: the prefix or the sequences' own tokens
-  int nt, waves;   // 16-row tiles of a wave; waves of k_kv_attn_tile, or 0 for k_kv_attn_rows
+  int nt, waves;   // 16-row tiles of a wave; waves of a workgroup
+  int tile;        // k_kv_attn_tile, not k_kv_attn_rows
   int row_tiles, slots, piece;
   int resident;    // workgroups that the chip holds at once
   float target;
@@ -988,8 +986,8 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 Part rows_part(const KvAttention &a, int64_t rows, int nt) {
   Part r = {};
   const bool wide = a.cache->head_dim > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
-  const int one = wide ? (f32 ? 1 : 2) : (f32 ? 3 : ROWS_OCC);
-  r.nt = nt;
+  const int one = wide ? (f32 ? 1 : 2) : (f32 ? 3 : 4);
+  r.nt = nt, r.waves = 4;
   r.resident = 256 * (nt == 1 ? one : (one + 1) / 2);
   r.row_tiles = (int)cdiv(rows, 16 * nt);
   return r;
@@ -1000,6 +998,7 @@ Part tile_part(const KvAttention &a, int64_t rows) {
   Part r = {};
   const int64_t hd = a.cache->head_dim;
   const bool wide = hd > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
+  r.tile = 1;
   r.nt = wide || f32 || rows <= 64 ? 1 : 2;
   r.waves = wide || rows <= 64 * r.nt ? 4 : 8;
   r.resident = 256 * (wide ? 1 : (hd > 64 || r.waves == 8 ? 8 / r.waves : 3));
@@ -1024,7 +1023,7 @@ Plan plan_of(const KvAttention &a) {
     p.prefix = plan_rows(a, a.tokens * G);
     // one launch for both lists where the prefix is so short that the own tokens' kernel does it
     // in one round of 128-token pieces
-    if (own && !p.own.waves) {
+    if (own && !p.own.tile) {
       const Part r = rows_part(a, a.tokens * G, p.own.nt);
       if (r.row_tiles * kvh * cdiv(a.prefix_len, 128) <= r.resident) p.prefix = r;
     }
@@ -1040,9 +1039,24 @@ Plan plan_of(const KvAttention &a) {
     const int64_t most = a.batch * cdiv(a.max_kv, 128);  // pieces of 128 tokens
     const float target = (float)r.resident / (float)units;
     r.slots = (int)a.batch;
+    // Short contexts: one piece a sequence, with more waves the fewer the sequences, saves the
+    // partial sums and the join (about 5 us); an iteration of such a workgroup costs about 2 us
+    // however little it reads, so the fewer workgroups there are to share the chip, the fewer
+    // iterations it may take. (32 heads of 128, 8 key/value heads: 30 x 6000 tokens 51.6 us cut
+    // into pieces, 44.7 us whole; 10 x 1000 13.4 and 12.1; 4 x 1000 10.7 and 11.5.)
+    if (!r.tile && r.nt == 1 && a.cache->head_dim <= 128 && a.dtype != NVFP4_DTYPE_F32 &&
+        a.prefix_len == 0) {
+      const int64_t n = a.batch * units, most_it = n / 20 < 1 ? 1 : n / 20 > 12 ? 12 : n / 20;
+      const int w = n <= 256 ? 16 : n <= 512 ? 8 : 4;
+      if (a.max_kv <= 32 * w * most_it) {
+        r.waves = w;
+        p.direct = 1;
+        return p;
+      }
+    }
     // many rows: a row's partial sums cost more than a workgroup's wait, so only where there
     // are far fewer workgroups than the chip holds
-    if (a.max_kv > 128 && target >= (r.waves ? 1.5f * (float)a.batch : 1.0f)) {
+    if (a.max_kv > 128 && target >= (r.tile ? 1.5f * (float)a.batch : 1.0f)) {
       r.target = target;
       const int64_t n = (int64_t)target + 1 + a.batch;
       r.slots = (int)(n < most ? n : most);
@@ -1054,18 +1068,25 @@ Plan plan_of(const KvAttention &a) {
 
 template <int HD, bool F32, bool EXACT>
 void launch_rows(const Attn &p, const Part &r, unsigned grid, hipStream_t st) {
-  const dim3 g(grid), b(256);
-  if (r.waves == 8) {
-    if constexpr (HD <= 128)
-      hipLaunchKernelGGL((k_kv_attn_tile<HD, F32 ? 1 : 2, F32, EXACT, 8>), g, dim3(512), 0, st, p);
-  } else if (r.waves == 4) {
-    if (r.nt == 1) hipLaunchKernelGGL((k_kv_attn_tile<HD, 1, F32, EXACT, 4>), g, b, 0, st, p);
-    else if constexpr (HD <= 128 && !F32)
+  const dim3 g(grid), b(64 * r.waves);
+  if (r.tile) {
+    if (r.waves == 8) {
+      if constexpr (HD <= 128)
+        hipLaunchKernelGGL((k_kv_attn_tile<HD, F32 ? 1 : 2, F32, EXACT, 8>), g, b, 0, st, p);
+    } else if (r.nt == 1) {
+      hipLaunchKernelGGL((k_kv_attn_tile<HD, 1, F32, EXACT, 4>), g, b, 0, st, p);
+    } else if constexpr (HD <= 128 && !F32) {
       hipLaunchKernelGGL((k_kv_attn_tile<HD, 2, F32, EXACT, 4>), g, b, 0, st, p);
+    }
+  } else if (r.waves > 4) {
+    if constexpr (HD <= 128 && !F32) {
+      if (r.waves == 16) hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT, 16>), g, b, 0, st, p);
+      else hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT, 8>), g, b, 0, st, p);
+    }
   } else if (r.nt == 1) {
-    hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT>), g, b, 0, st, p);
-  } else {
-    hipLaunchKernelGGL((k_kv_attn_rows<HD, 2, F32, EXACT>), g, b, 0, st, p);
+    hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT, 4>), g, b, 0, st, p);
+  } else if constexpr (HD <= 128 || !F32) {
+    hipLaunchKernelGGL((k_kv_attn_rows<HD, 2, F32, EXACT, 4>), g, b, 0, st, p);
   }
 }
 
@@ -1155,7 +1176,7 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
     else launch_hd<false>(p, parts[k], g, st);
   };
   const bool both = grids[0] && grids[1] && parts[0].nt == parts[1].nt &&
-                    parts[0].waves == parts[1].waves && grids[0] + grids[1] <= INT32_MAX;
+                    parts[0].waves == parts[1].waves && parts[0].tile == parts[1].tile && grids[0] + grids[1] <= INT32_MAX;
   if (grids[0]) launch(0, both);
   if (grids[1] && !both) launch(1, false);
   if (!plan.direct) {
