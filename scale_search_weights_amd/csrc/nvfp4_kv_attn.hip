@@ -31,6 +31,12 @@ typedef unsigned u4 __attribute__((ext_vector_type(4)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
+#ifndef HF
+#define HF 0.75f
+#endif
+#ifndef LEAST
+#define LEAST 3
+#endif
 constexpr float kLn2 = 0.6931471805599453f;
 
 // A token list and the query rows that read it: the shared prefix (all rows of the call over one
@@ -419,6 +425,12 @@ template <bool F32>
 __device__ __forceinline__ void store_out(void *out, int64_t e, float a, float b) {
   if (F32) *reinterpret_cast<float2 *>(static_cast<float *>(out) + e) = make_float2(a, b);
   else *reinterpret_cast<unsigned *>(static_cast<uint16_t *>(out) + e) = bf16x2_bits(a, b);
+}
+
+template <bool F32>
+__device__ __forceinline__ void store4(void *out, int64_t e, f4 y) {
+  if (F32) *reinterpret_cast<f4 *>(static_cast<float *>(out) + e) = y;
+  else *reinterpret_cast<u2 *>(static_cast<uint16_t *>(out) + e) = (u2){bf16x2_bits(y[0], y[1]), bf16x2_bits(y[2], y[3])};
 }
 
 // ---------------------------------------------------------------- query rows of a wave
@@ -860,12 +872,13 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
       const int ch = DV * (4 * quad + r4);
       if (EXACT || ch < p.hd) {
 #pragma unroll
-        for (int d = 0; d < DV; d += 2) {
-          const float a = x.acc[n][d][r4] * f, b = x.acc[n][d + 1][r4] * f;
+        for (int d = 0; d < DV; d += 4) {
+          const f4 y = {x.acc[n][d][r4] * f, x.acc[n][d + 1][r4] * f, x.acc[n][d + 2][r4] * f,
+                        x.acc[n][d + 3][r4] * f};
           if (sh.direct)
-            store_out<F32>(p.out, at * p.hd + ch + d, a, b);
+            store4<F32>(p.out, at * p.hd + ch + d, y);
           else
-            *reinterpret_cast<float2 *>(p.list[sh.list].opart + (part + r) * p.hd + ch + d) = make_float2(a, b);
+            *reinterpret_cast<f4 *>(p.list[sh.list].opart + (part + r) * p.hd + ch + d) = y;
         }
       }
     }
@@ -957,8 +970,7 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
   const int64_t to = (int64_t)(lo + i) * p.heads + head;
   const float f = L > 0.0f ? p.S_v[h] / L : 0.0f;
   if (in) {
-    store_out<F32>(p.out, to * p.hd + 4 * c, y[0] * f, y[1] * f);
-    store_out<F32>(p.out, to * p.hd + 4 * c + 2, y[2] * f, y[3] * f);
+    store4<F32>(p.out, to * p.hd + 4 * c, y * f);
   }
   if (c == 0 && p.lse) p.lse[to] = L > 0.0f ? kLn2 * (M + __builtin_amdgcn_logf(L)) : -INFINITY;
 }
@@ -1036,29 +1048,29 @@ Plan plan_of(const KvAttention &a) {
   if (own) {
     Part &r = p.own;
     const int64_t units = kvh * r.row_tiles;
-    const int64_t most = a.batch * cdiv(a.max_kv, 128);  // pieces of 128 tokens
-    const float target = (float)r.resident / (float)units;
+    // pieces wanted: with the half piece that a sequence adds on average, as many as the chip
+    // holds at once (64 sequences of 512 to 8192 tokens: 55 -> 49 us against not counting it)
+    const float held = (float)r.resident / (float)units;
+    const float target = fmaxf(held - 0.5f * (float)a.batch, HF * held);
     r.slots = (int)a.batch;
     // Short contexts: one piece a sequence, with more waves the fewer the sequences, saves the
     // partial sums and the join (about 5 us); an iteration of such a workgroup costs about 2 us
     // however little it reads, so the fewer workgroups there are to share the chip, the fewer
     // iterations it may take. (32 heads of 128, 8 key/value heads: 30 x 6000 tokens 51.6 us cut
     // into pieces, 44.7 us whole; 10 x 1000 13.4 and 12.1; 4 x 1000 10.7 and 11.5.)
+    bool whole = a.max_kv <= 128;
     if (!r.tile && r.nt == 1 && a.cache->head_dim <= 128 && a.dtype != NVFP4_DTYPE_F32 &&
-        a.prefix_len == 0) {
-      const int64_t n = a.batch * units, most_it = n / 20 < 1 ? 1 : n / 20 > 12 ? 12 : n / 20;
+        !(p.prefix.slots && !p.prefix.tile)) {
+      const int64_t n = a.batch * units, most = n / 20 < LEAST ? LEAST : n / 20 > 12 ? 12 : n / 20;
       const int w = n <= 256 ? 16 : n <= 512 ? 8 : 4;
-      if (a.max_kv <= 32 * w * most_it) {
-        r.waves = w;
-        p.direct = 1;
-        return p;
-      }
+      whole = a.max_kv <= 32 * w * most;
+      if (whole) r.waves = w;
     }
     // many rows: a row's partial sums cost more than a workgroup's wait, so only where there
     // are far fewer workgroups than the chip holds
-    if (a.max_kv > 128 && target >= (r.tile ? 1.5f * (float)a.batch : 1.0f)) {
+    if (!whole && held >= (r.tile ? 1.5f * (float)a.batch : 1.0f)) {
       r.target = target;
-      const int64_t n = (int64_t)target + 1 + a.batch;
+      const int64_t n = (int64_t)target + 1 + a.batch, most = a.batch * cdiv(a.max_kv, 128);
       r.slots = (int)(n < most ? n : most);
     }
   }

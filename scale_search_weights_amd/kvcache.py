@@ -80,6 +80,7 @@ class KVCache:
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, size, 2 * half
         self.device = k_codes.device
         self._index = self.device.index
+        self._needs = {}  # attention's workspace size by the sizes of a call
         self._c = _Cache(*(t.data_ptr() for t in (k_codes, k_scales, v_codes, v_scales, S_k, S_v)),
                          pages, size, heads, 2 * half)
         self._ref = ctypes.addressof(self._c)
@@ -144,7 +145,7 @@ def write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor)
     _ids(slots, "slots", cache, 1, _INT64)
     if slots.shape[0] != n:
         raise ValueError(f"slots must have {n} elements, got {slots.shape[0]}")
-    _check(lib().nvfp4_kv_write(cache._ref, k.data_ptr(), v.data_ptr(), dt, n, k_ts, k_hs,
+    _check((_bound or lib()).nvfp4_kv_write(cache._ref, k.data_ptr(), v.data_ptr(), dt, n, k_ts, k_hs,
                                 v_ts, v_hs, slots.data_ptr(), _raw_stream(cache._index)), "nvfp4_kv_write")
 
 
@@ -157,7 +158,7 @@ def read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat1
     n = slots.shape[0]
     k = torch.empty((n, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
     v = torch.empty_like(k)
-    _check(lib().nvfp4_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _dt(k),
+    _check((_bound or lib()).nvfp4_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _dt(k),
                                _raw_stream(cache._index)), "nvfp4_kv_read")
     return k, v
 
@@ -234,9 +235,13 @@ def attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor | None 
     else:
         _arg(out, "out", q, q.dtype, numel=q.numel())
     lse = torch.empty(tokens, heads, dtype=torch.float32, device=q.device) if return_lse else None
-    L = lib()
-    need = L.nvfp4_kv_attention_workspace_size(cache._ref, dt, tokens, heads, batch, max_q, max_kv,
-                                               prefix_len)
+    L = _bound or lib()
+    sizes = (dt, tokens, heads, batch, max_q, max_kv, prefix_len)
+    need = cache._needs.get(sizes)
+    if need is None:
+        if len(cache._needs) >= 4096:
+            cache._needs.clear()
+        need = cache._needs[sizes] = L.nvfp4_kv_attention_workspace_size(cache._ref, *sizes)
     if workspace is not None:
         _arg(workspace, "workspace", cache.k_codes, torch.uint8, min_numel=need)
     elif need:
