@@ -451,55 +451,64 @@ struct Rows {
   f4 acc[NT][HD / 16];             // channel (4 quad + r) HD/16 + d of row i in acc[n][d][r]
 };
 
+// Issue the loads of the lane's share of the rows; use_rows makes operands of them when other
+// loads are on their way too.
+template <int HD, int NT, bool F32>
+struct RawRows {
+  u4 q[NT][HD / 32][F32 ? 2 : 1];
+};
+
 template <int HD, int NT, bool F32, bool EXACT>
 __device__ __forceinline__ void load_rows(const Attn &p, const Job &j, int h, int r0, int rows,
-                                          int lane, Rows<HD, NT, F32> &x) {
+                                          int lane, RawRows<HD, NT, F32> &y, Rows<HD, NT, F32> &x) {
   const int i = lane & 15, quad = lane >> 4;
-  const float sc = p.scale * kLog2e * p.S_k[h];
-  const float sign = sc < 0.0f ? -1.0f : 1.0f;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int r = min(r0 + 16 * n + i, rows - 1);
     const int tok = r / p.group, head = h * p.group + (r - tok * p.group);
     x.lim[n] = j.causal ? min(j.len, j.len - j.nq + tok + 1) : j.len;
     const int64_t at = (int64_t)(j.q0 + tok) * p.q_ts + head * p.q_hs + quad * (HD / 4);
+#pragma unroll
+    for (int s = 0; s < HD / 32; ++s)
+#pragma unroll
+      for (int w = 0; w < (F32 ? 2 : 1); ++w) {
+        y.q[n][s][w] = (u4){0, 0, 0, 0};
+        if (EXACT || quad * (HD / 4) + 8 * s < p.hd)
+          y.q[n][s][w] = F32 ? *reinterpret_cast<const u4 *>(static_cast<const float *>(p.q) + at + 8 * s + 4 * w)
+                             : *reinterpret_cast<const u4 *>(static_cast<const uint16_t *>(p.q) + at + 8 * s);
+      }
+  }
+}
+
+template <int HD, int NT, bool F32>
+__device__ __forceinline__ void use_rows(const RawRows<HD, NT, F32> &y, float scale, Rows<HD, NT, F32> &x) {
+  const float sign = scale < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
     float v[HD / 4], amax = 0.0f;
 #pragma unroll
-    for (int s = 0; s < HD / 32; ++s) {
-      if (EXACT || quad * (HD / 4) + 8 * s < p.hd) {
-        if (F32) {
-          const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at + 8 * s);
-          const float4 a = f[0], b = f[1];
-          v[8 * s] = a.x, v[8 * s + 1] = a.y, v[8 * s + 2] = a.z, v[8 * s + 3] = a.w;
-          v[8 * s + 4] = b.x, v[8 * s + 5] = b.y, v[8 * s + 6] = b.z, v[8 * s + 7] = b.w;
-        } else {
-          const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at + 8 * s);
-          v[8 * s] = bf16_lo(a.x), v[8 * s + 1] = bf16_hi(a.x), v[8 * s + 2] = bf16_lo(a.y);
-          v[8 * s + 3] = bf16_hi(a.y), v[8 * s + 4] = bf16_lo(a.z), v[8 * s + 5] = bf16_hi(a.z);
-          v[8 * s + 6] = bf16_lo(a.w), v[8 * s + 7] = bf16_hi(a.w);
-        }
-      } else {
+    for (int s = 0; s < HD / 32; ++s)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * s + e] = 0.0f;
+      for (int e = 0; e < 8; ++e) {
+        if (F32) v[8 * s + e] = __uint_as_float(y.q[n][s][F32 ? e >> 2 : 0][e & 3]);
+        else v[8 * s + e] = e & 1 ? bf16_hi(y.q[n][s][0][e >> 1]) : bf16_lo(y.q[n][s][0][e >> 1]);
+        amax = fmaxf(amax, fabsf(v[8 * s + e]));
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[8 * s + e]));
-    }
     amax = fmaxf(amax, xor16(amax));
     amax = fmaxf(amax, xor32(amax));
     float inv;
     const float f = row_factor(amax, inv) * sign;
-    x.c[n] = fmaxf(fabsf(sc) * inv, 1e-37f);  // positive, so a hidden score stays -inf
+    x.c[n] = fmaxf(fabsf(scale) * inv, 1e-37f);  // positive, so a hidden score stays -inf
     x.off[n] = INFINITY;
     x.l[n] = 0.0f;
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float y = v[8 * s + e] * f;
-        const _Float16 hi = (_Float16)y;
+        const float z = v[8 * s + e] * f;
+        const _Float16 hi = (_Float16)z;
         x.q[n][0][s][e] = hi;
-        if (F32) x.q[n][F32 ? 1 : 0][s][e] = (_Float16)(y - (float)hi);
+        if (F32) x.q[n][F32 ? 1 : 0][s][e] = (_Float16)(z - (float)hi);
       }
 #pragma unroll
     for (int d = 0; d < HD / 16; ++d) x.acc[n][d] = (f4){0, 0, 0, 0};
@@ -601,6 +610,7 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
   const Job j = sh.j;
   const int h = sh.h, rows = j.nq * p.group, r0 = sh.rt * (16 * NT), t0 = sh.t0;
   if (r0 >= rows) return;
+  const float S_k = p.S_k[h], S_v = p.S_v[h];
   int t1 = sh.t1;
 
   int lim_lo, lim_hi;
@@ -611,12 +621,18 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
   int ok = 0, nxt_ok = 0;
   Pages pg = open_pages(j, p.page_shift, t0, t1, lane);
   Rows<HD, NT, F32> x;
-  load_rows<HD, NT, F32, EXACT>(p, j, h, r0, rows, lane, x);
   int t = t0 + 32 * wave;
-  if (t < t1) {
+  {
+    RawRows<HD, NT, F32> raw;
+    load_rows<HD, NT, F32, EXACT>(p, j, h, r0, rows, lane, raw, x);
+    __builtin_amdgcn_sched_barrier(0);
+    if (t < t1) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-      ok |= load_group<HD, EXACT>(p, page_of(pg, t + 16 * u), h, t + 16 * u, lane, g[u]) << u;
+      for (int u = 0; u < 2; ++u)
+        ok |= load_group<HD, EXACT>(p, page_of(pg, t + 16 * u), h, t + 16 * u, lane, g[u]) << u;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    use_rows<HD, NT, F32>(raw, p.scale * kLog2e * S_k, x);
   }
   for (; t < t1; advance(pg, j, p.page_shift, t1, lane))
   for (const int te = min(t1, pg.t + kRun); t < te; t += 32 * W) {
@@ -688,7 +704,6 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
     if (quad == 0) sm_m[wave][16 * n + i] = kBase - x.off[n], sm_l[wave][16 * n + i] = x.l[n];
   }
   __syncthreads();
-  const float S_v = p.S_v[h];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float M = -INFINITY;
@@ -762,6 +777,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   const Job j = sh.j;
   const int h = sh.h, rows = j.nq * p.group, R0 = sh.rt * (16 * NT * W), t0 = sh.t0;
   if (R0 >= rows) return;
+  const float S_k = p.S_k[h], S_v = p.S_v[h];
   int t1 = sh.t1;
   const int r0 = R0 + wave * 16 * NT;
 
@@ -793,9 +809,15 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
       reinterpret_cast<h4 *>(&vfrag[b][wave >> 1][d][lane])[wave & 1] = vf[d];
     order_wave_lds();
   };
-  if (t0 < t1) fetch(t0);
   Rows<HD, NT, F32> x;
-  load_rows<HD, NT, F32, EXACT>(p, j, h, r0, rows, lane, x);
+  {
+    RawRows<HD, NT, F32> raw;
+    load_rows<HD, NT, F32, EXACT>(p, j, h, r0, rows, lane, raw, x);
+    __builtin_amdgcn_sched_barrier(0);
+    if (t0 < t1) fetch(t0);
+    __builtin_amdgcn_sched_barrier(0);
+    use_rows<HD, NT, F32>(raw, p.scale * kLog2e * S_k, x);
+  }
   if (t0 < t1) {
     dequantise(0);
     if (t0 + STAGE < t1) fetch(t0 + STAGE);
@@ -856,7 +878,6 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
 
   // each lane holds HD/16 consecutive channels of its row four times
   const int64_t part = part_of(p, sh);
-  const float S_v = p.S_v[h];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float l = x.l[n];
@@ -931,6 +952,7 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
   }
   const bool here = lo + i < hi;
   const int h = head / p.group, gr = head - h * p.group;
+  const float S_v = p.S_v[h];
   const int64_t rows = (int64_t)p.tokens * p.group, own_rows = (int64_t)p.max_q * p.group;
   const int64_t at = h * rows + (int64_t)(lo + i) * p.group + gr;      // in a prefix slot
   const int64_t own_at = ((int64_t)own0 * p.kv_heads + h) * own_rows + (int64_t)i * p.group + gr;
@@ -968,7 +990,7 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
     y += so[g + k][c] * e;
   }
   const int64_t to = (int64_t)(lo + i) * p.heads + head;
-  const float f = L > 0.0f ? p.S_v[h] / L : 0.0f;
+  const float f = L > 0.0f ? S_v / L : 0.0f;
   if (in) {
     store4<F32>(p.out, to * p.hd + 4 * c, y * f);
   }
