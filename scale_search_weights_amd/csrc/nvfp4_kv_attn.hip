@@ -31,12 +31,6 @@ typedef unsigned u4 __attribute__((ext_vector_type(4)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
-#ifndef HF
-#define HF 0.75f
-#endif
-#ifndef LEAST
-#define LEAST 3
-#endif
 constexpr float kLn2 = 0.6931471805599453f;
 
 // A token list and the query rows that read it: the shared prefix (all rows of the call over one
@@ -75,7 +69,8 @@ struct Job {
   const int32_t *pages;
 };
 
-__device__ __forceinline__ Job job_of(const Attn &p, const List &k, int b) {
+// len: the sequence's own tokens (not of the prefix's job).
+__device__ __forceinline__ Job job_of(const Attn &p, const List &k, int b, int len) {
   Job j;
   if (k.prefix) {
     j.q0 = 0, j.nq = p.tokens, j.len = k.max_len, j.causal = 0, j.pages = k.table;
@@ -86,7 +81,7 @@ __device__ __forceinline__ Job job_of(const Attn &p, const List &k, int b) {
       hi = min(max(p.q_offsets[b + 1], lo), min(p.tokens, lo + p.max_q));
     }
     j.q0 = lo, j.nq = hi - lo;
-    j.len = p.kv_lens ? min(max(p.kv_lens[b], 0), k.max_len) : 0;
+    j.len = len;
     j.causal = k.causal;
     j.pages = k.table + b * k.table_width;
   }
@@ -115,36 +110,38 @@ __device__ __forceinline__ T prefix_sum(T x) {
 // all sequences, so the grid has few workgroups without work however unequal the lengths
 // are. Every wave finds its piece by itself: two passes over the lengths.
 struct Piece {
-  int b, first, count, tokens;  // sequence, its first slot, its pieces, tokens of each
+  int b, first, count, tokens, len;  // sequence, its first slot, its pieces, tokens of each; its length
 };
 
-__device__ __forceinline__ int units_of(const int32_t *kv_lens, int b, int max_len) {
-  return (min(max(kv_lens[b], 0), max_len) + 127) >> 7;
+__device__ __forceinline__ int length_of(const int32_t *kv_lens, int b, int batch, int max_len) {
+  return b < batch ? min(max(kv_lens[b], 0), max_len) : 0;
 }
 
 // The piece of `slot`; b = -1: there is none.
 __device__ __forceinline__ Piece find_piece(const int32_t *kv_lens, int batch, int max_len,
                                             float target, int slot, int lane) {
-  float sum = 0.0f;
-  for (int b = lane; b < batch; b += 64) sum += (float)units_of(kv_lens, b, max_len);
+  const int mine = length_of(kv_lens, lane, batch, max_len);  // the only load for 64 sequences
+  float sum = (float)(mine + 127 >> 7);
+  for (int b = lane + 64; b < batch; b += 64)
+    sum += (float)(length_of(kv_lens, b, batch, max_len) + 127 >> 7);
   sum = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(prefix_sum(sum)), 63));
   const float x = ceilf(sum / target);  // the same in every wave: same order, same bits
   const int per = x < 1.0f ? 1 : (x > 8388608.0f ? 8388608 : (int)x);
-  Piece r = {-1, 0, 0, 0};
+  Piece r = {-1, 0, 0, 0, 0};
   int before = 0;
   for (int b0 = 0; b0 < batch; b0 += 64) {
-    const int b = b0 + lane;
-    const int n = b < batch ? (units_of(kv_lens, b, max_len) + per - 1) / per : 0;
+    const int len = b0 ? length_of(kv_lens, b0 + lane, batch, max_len) : mine;
+    const int n = ((len + 127 >> 7) + per - 1) / per;
     const int upto = prefix_sum(n);
     const unsigned long long hit =
         __ballot(slot >= before + upto - n && slot < before + upto);
     if (hit) {
       const int at = __builtin_ctzll(hit);
       r.b = b0 + at;
+      r.len = __builtin_amdgcn_readlane(len, at);
       r.count = __builtin_amdgcn_readlane(n, at);
       r.first = before + __builtin_amdgcn_readlane(upto, at) - r.count;
-      const int units = units_of(kv_lens, r.b, max_len);
-      r.tokens = (units + r.count - 1) / r.count << 7;
+      r.tokens = ((r.len + 127 >> 7) + r.count - 1) / r.count << 7;
       return r;
     }
     before += __builtin_amdgcn_readlane(upto, 63);
@@ -178,7 +175,8 @@ __device__ __forceinline__ bool share_of(const Attn &p, int lane, Share &s) {
   const int slot = w / k.row_tiles;
   s.direct = p.direct;
   if (k.prefix || k.target == 0.0f) {
-    s.j = job_of(p, k, k.prefix ? 0 : slot);
+    const int len = k.prefix || !p.kv_lens ? 0 : length_of(p.kv_lens, slot, p.batch, k.max_len);
+    s.j = job_of(p, k, k.prefix ? 0 : slot, len);
     s.t0 = k.prefix ? slot * k.piece : 0;
     s.t1 = k.prefix ? min(s.j.len, s.t0 + k.piece) : s.j.len;
   } else {
@@ -187,7 +185,7 @@ __device__ __forceinline__ bool share_of(const Attn &p, int lane, Share &s) {
     s.direct = x.count == 1 && !k.joined;  // the join skips such sequences
     if (slot == x.first && s.h == 0 && s.rt == 0 && threadIdx.x == 0)
       k.where[x.b] = make_int2(x.first, x.count);  // for the join
-    s.j = job_of(p, k, x.b);
+    s.j = job_of(p, k, x.b, x.len);
     s.t0 = (slot - x.first) * x.tokens;
     s.t1 = min(s.j.len, s.t0 + x.tokens);
   }
@@ -1028,13 +1026,17 @@ Part rows_part(const KvAttention &a, int64_t rows, int nt) {
 }
 
 // k_kv_attn_tile: workgroups a CU holds, by LDS (at HD 256 1 KiB a token, two stages).
-Part tile_part(const KvAttention &a, int64_t rows) {
+// Calls that tiles of 256 rows and pieces of 128 tokens would give fewer than 512 workgroups
+// take tiles of 64 rows (240 rows x 700 tokens of 8 heads 22.7 -> 17.0 us, 2000 x 2500 32 -> 29;
+// from 512 workgroups on equal or slower).
+Part tile_part(const KvAttention &a, int64_t rows, int64_t jobs, int64_t len) {
   Part r = {};
+  const bool small = jobs * a.cache->kv_heads * cdiv(rows, 256) * cdiv(len, 128) < 512;
   const int64_t hd = a.cache->head_dim;
   const bool wide = hd > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
   r.tile = 1;
-  r.nt = wide || f32 || rows <= 64 ? 1 : 2;
-  r.waves = wide || rows <= 64 * r.nt ? 4 : 8;
+  r.nt = wide || f32 || small || rows <= 64 ? 1 : 2;
+  r.waves = wide || small || rows <= 64 * r.nt ? 4 : 8;
   r.resident = 256 * (wide ? 1 : (hd > 64 || r.waves == 8 ? 8 / r.waves : 3));
   r.row_tiles = (int)cdiv(rows, 16 * r.nt * r.waves);
   return r;
@@ -1042,8 +1044,8 @@ Part tile_part(const KvAttention &a, int64_t rows) {
 
 // Rows a (sequence, key/value head): up to 32 to k_kv_attn_rows, whose waves work alone; more to
 // k_kv_attn_tile, whose waves share what they dequantise.
-Part plan_rows(const KvAttention &a, int64_t rows) {
-  if (rows > 32) return tile_part(a, rows);
+Part plan_rows(const KvAttention &a, int64_t rows, int64_t jobs, int64_t len) {
+  if (rows > 32) return tile_part(a, rows, jobs, len);
   const bool one = rows <= 16 || (a.cache->head_dim > 128 && a.dtype == NVFP4_DTYPE_F32);
   return rows_part(a, rows, one ? 1 : 2);
 }
@@ -1052,9 +1054,9 @@ Plan plan_of(const KvAttention &a) {
   Plan p = {};
   const int64_t G = a.heads / a.cache->kv_heads, kvh = a.cache->kv_heads;
   const bool own = a.max_kv > 0 || a.prefix_len == 0;
-  if (own) p.own = plan_rows(a, a.max_q * G);
+  if (own) p.own = plan_rows(a, a.max_q * G, a.batch, a.max_kv);
   if (a.prefix_len > 0) {
-    p.prefix = plan_rows(a, a.tokens * G);
+    p.prefix = plan_rows(a, a.tokens * G, 1, a.prefix_len);
     // one launch for both lists where the prefix is so short that the own tokens' kernel does it
     // in one round of 128-token pieces
     if (own && !p.own.tile) {
@@ -1073,7 +1075,7 @@ Plan plan_of(const KvAttention &a) {
     // pieces wanted: with the half piece that a sequence adds on average, as many as the chip
     // holds at once (64 sequences of 512 to 8192 tokens: 55 -> 49 us against not counting it)
     const float held = (float)r.resident / (float)units;
-    const float target = fmaxf(held - 0.5f * (float)a.batch, HF * held);
+    const float target = fmaxf(held - 0.5f * (float)a.batch, 0.75f * held);
     r.slots = (int)a.batch;
     // Short contexts: one piece a sequence, with more waves the fewer the sequences, saves the
     // partial sums and the join (about 5 us); an iteration of such a workgroup costs about 2 us
@@ -1083,7 +1085,7 @@ Plan plan_of(const KvAttention &a) {
     bool whole = a.max_kv <= 128;
     if (!r.tile && r.nt == 1 && a.cache->head_dim <= 128 && a.dtype != NVFP4_DTYPE_F32 &&
         !(p.prefix.slots && !p.prefix.tile)) {
-      const int64_t n = a.batch * units, most = n / 20 < LEAST ? LEAST : n / 20 > 12 ? 12 : n / 20;
+      const int64_t n = a.batch * units, most = n / 20 < 3 ? 3 : n / 20 > 12 ? 12 : n / 20;
       const int w = n <= 256 ? 16 : n <= 512 ? 8 : 4;
       whole = a.max_kv <= 32 * w * most;
       if (whole) r.waves = w;
