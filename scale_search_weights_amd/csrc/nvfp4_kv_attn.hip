@@ -14,9 +14,17 @@
 // of the cache: lane (i, quad) takes channels [quad HD/4, ..) of key token i, and channels
 // [i HD/16, ..) of the value tokens 4 quad + 0..3 and 16 + 4 quad + 0..3.
 //
+// Two kernels. With up to 32 rows a (sequence, key/value head) the cache is read at the rate of
+// memory: k_kv_attn_rows, every wave dequantising its own tokens in registers (about 250 vector
+// instructions for 32 tokens and 16 rows; 524000 tokens of 8 heads of 128, 604 MB, in 117 us,
+// 5.2 TB/s). With more rows the products bound it: k_kv_attn_tile, where the waves share what they
+// dequantise through LDS (2 x 2048 queries of 32 heads on 8192 tokens, 481 GFLOP, in 430 us,
+// 1.1 PFLOP/s). The sequence axis is cut into pieces where there are few rows, and
+// k_kv_attn_join joins their sums in a fixed order.
+//
 // Running maximum: it is raised (and the sums rescaled) only when a probability relative to it
 // leaves fp16's range, a few times per sequence instead of once per tile, and no maximum is
-// taken in between: the sums show the overflow.
+// taken in between: the sums show the overflow (2048-query chunk 577 -> 560 us).
 #include "nvfp4_device.h"
 #include "nvfp4_kv.h"
 
@@ -106,11 +114,12 @@ __device__ __forceinline__ T prefix_sum(T x) {
 
 // The sequences' own tokens are cut into pieces of at most a length chosen from the lengths found
 // on the device so that about `target` pieces come out in all (at most target + batch: every
-// sequence may add one that is not full); a sequence's pieces are equal, in units of 128. Slots number the pieces over
-// all sequences, so the grid has few workgroups without work however unequal the lengths
-// are. Every wave finds its piece by itself: two passes over the lengths.
+// sequence may add one that is not full); a sequence's pieces are equal, in units of 128 tokens.
+// Slots number the pieces over all sequences, so the grid has few workgroups without work however
+// unequal the lengths are. Every wave finds its piece by itself: two passes over the lengths.
+// (64 sequences of 512 to 8192 tokens: 92 us with pieces of one length for the bound, 60 us so.)
 struct Piece {
-  int b, first, count, tokens, len;  // sequence, its first slot, its pieces, tokens of each; its length
+  int b, first, count, tokens, len;  // sequence, its first slot, pieces, tokens of each, length
 };
 
 __device__ __forceinline__ int length_of(const int32_t *kv_lens, int b, int batch, int max_len) {
@@ -156,10 +165,13 @@ struct Share {
   int h, rt, t0, t1, direct, list, slot;
 };
 
-// the first partial row of the job
+// The job's first partial row. A slot holds the rows of all tokens (prefix), of one sequence (own
+// tokens in pieces), or, of own tokens in one piece, the rows of all tokens are one slot.
 __device__ __forceinline__ int64_t part_of(const Attn &p, const Share &s) {
-  const int rows = p.list[s.list].prefix ? p.tokens * p.group : p.max_q * p.group;
-  return ((int64_t)s.slot * p.kv_heads + s.h) * rows;
+  const List &k = p.list[s.list];
+  if (k.prefix || k.target > 0.0f)
+    return ((int64_t)s.slot * p.kv_heads + s.h) * ((k.prefix ? p.tokens : p.max_q) * p.group);
+  return ((int64_t)s.h * p.tokens + s.j.q0) * p.group;
 }
 
 __device__ __forceinline__ bool share_of(const Attn &p, int lane, Share &s) {
@@ -269,8 +281,6 @@ __device__ __forceinline__ int page_of(const Pages &pg, int t) {
   return __builtin_amdgcn_readlane(pg.next, g - kRun / 16);
 }
 
-// Loads the group at t of page `id`; returns whether the page is one of the cache's. A group
-// that is not there is read from page 0 and never used.
 #define GLOBAL __attribute__((address_space(1)))
 
 // An unsigned lane offset that stays 32 bits beside a scalar base address (hoisted out of a loop
@@ -280,6 +290,8 @@ __device__ __forceinline__ unsigned lane_offset(unsigned o) {
   return o;
 }
 
+// Loads the group at t of page `id`; returns whether the page is one of the cache's. A group
+// that is not there is read from page 0 and never used.
 template <int HD, bool EXACT>
 __device__ __forceinline__ int load_group(const Attn &p, int id, int h, int t, int lane, Group<HD> &x) {
   // uniform base addresses and unsigned lane offsets
@@ -428,7 +440,8 @@ __device__ __forceinline__ void store_out(void *out, int64_t e, float a, float b
 template <bool F32>
 __device__ __forceinline__ void store4(void *out, int64_t e, f4 y) {
   if (F32) *reinterpret_cast<f4 *>(static_cast<float *>(out) + e) = y;
-  else *reinterpret_cast<u2 *>(static_cast<uint16_t *>(out) + e) = (u2){bf16x2_bits(y[0], y[1]), bf16x2_bits(y[2], y[3])};
+  else *reinterpret_cast<u2 *>(static_cast<uint16_t *>(out) + e) =
+      (u2){bf16x2_bits(y[0], y[1]), bf16x2_bits(y[2], y[3])};
 }
 
 // ---------------------------------------------------------------- query rows of a wave
@@ -633,7 +646,7 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
     use_rows<HD, NT, F32>(raw, p.scale * kLog2e * S_k, x);
   }
   for (; t < t1; advance(pg, j, p.page_shift, t1, lane))
-  for (const int te = min(t1, pg.t + kRun); t < te; t += 32 * W) {
+  for (const int te = min(t1, pg.t + kRun); t < te; t += 32 * W) {  // the tiles of a run
     if (t + 32 * W < t1) {
       nxt_ok = 0;
 #pragma unroll
@@ -759,7 +772,9 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
 // are in LDS, so the next one is dequantised beside the products of this one by whichever
 // wave comes to it. Score products run at a raised wave priority: of a SIMD's two waves, one in
 // its products then goes ahead of one in its exponentials, which fills the gaps between
-// them.
+// them (468 -> 444 us on two 2048-query chunks; at both products the same, at the second alone
+// 460). Eight waves: four (half the rows a dequantised group serves) take 515 us. The products
+// alone would take 257 us, the exponentials add about 100, dequantising 60, LDS reads 30.
 template <int HD, int NT, bool F32, bool EXACT, int W>
 __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, KS = HD / 32, STAGE = 16 * W;
@@ -823,7 +838,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   __syncthreads();
   int b = 0, t = t0;
   for (; t < t1; advance(pg, j, p.page_shift, t1, lane))
-  for (const int te = min(t1, pg.t + kRun); t < te; t += STAGE, b ^= 1) {
+  for (const int te = min(t1, pg.t + kRun); t < te; t += STAGE, b ^= 1) {  // the stages of a run
     // operands are read one step ahead of their products: the values' before the exponentials,
     // the next tile's keys before the second product
     const int tiles = min(W / 2, (min(t1, lim_hi) - t + 31) >> 5);
@@ -938,7 +953,7 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
     lo = min(max(p.q_offsets[b], 0), p.tokens);
     hi = min(max(p.q_offsets[b + 1], lo), min(p.tokens, lo + p.max_q));
   }
-  int own0 = b, n = p.n_prefix;
+  int own0 = 0, n = p.n_prefix;
   if (p.where) {
     if (p.kv_lens[b] > 0) {
       const int2 x = p.where[b];
@@ -952,8 +967,9 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
   const int h = head / p.group, gr = head - h * p.group;
   const float S_v = p.S_v[h];
   const int64_t rows = (int64_t)p.tokens * p.group, own_rows = (int64_t)p.max_q * p.group;
-  const int64_t at = h * rows + (int64_t)(lo + i) * p.group + gr;      // in a prefix slot
-  const int64_t own_at = ((int64_t)own0 * p.kv_heads + h) * own_rows + (int64_t)i * p.group + gr;
+  const int64_t at = h * rows + (int64_t)(lo + i) * p.group + gr;  // in a slot of all tokens
+  const int64_t own_at =
+      p.where ? ((int64_t)own0 * p.kv_heads + h) * own_rows + (int64_t)i * p.group + gr : at;
   const int64_t step = rows * p.kv_heads, own_step = own_rows * p.kv_heads;
   float M = -INFINITY, L = 0.0f;
   f4 y = {0, 0, 0, 0};
@@ -989,9 +1005,7 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
   }
   const int64_t to = (int64_t)(lo + i) * p.heads + head;
   const float f = L > 0.0f ? S_v / L : 0.0f;
-  if (in) {
-    store4<F32>(p.out, to * p.hd + 4 * c, y * f);
-  }
+  if (in) store4<F32>(p.out, to * p.hd + 4 * c, y * f);
   if (c == 0 && p.lse) p.lse[to] = L > 0.0f ? kLn2 * (M + __builtin_amdgcn_logf(L)) : -INFINITY;
 }
 
@@ -1018,7 +1032,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 Part rows_part(const KvAttention &a, int64_t rows, int nt) {
   Part r = {};
   const bool wide = a.cache->head_dim > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
-  const int one = wide ? (f32 ? 1 : 2) : (f32 ? 3 : 4);
+  const int one = wide ? 2 : (f32 ? 3 : 4);
   r.nt = nt, r.waves = 4;
   r.resident = 256 * (nt == 1 ? one : (one + 1) / 2);
   r.row_tiles = (int)cdiv(rows, 16 * nt);
@@ -1148,7 +1162,8 @@ int64_t prefix_rows(const KvAttention &a, const Plan &p) {
   return (int64_t)p.prefix.slots * a.tokens * a.heads;
 }
 int64_t own_rows(const KvAttention &a, const Plan &p) {
-  return (int64_t)p.own.slots * a.max_q * a.heads;
+  if (p.own.target > 0.0f) return (int64_t)p.own.slots * a.max_q * a.heads;
+  return p.own.slots ? a.tokens * a.heads : 0;
 }
 
 template <int HD>
@@ -1212,7 +1227,8 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
     else launch_hd<false>(p, parts[k], g, st);
   };
   const bool both = grids[0] && grids[1] && parts[0].nt == parts[1].nt &&
-                    parts[0].waves == parts[1].waves && parts[0].tile == parts[1].tile && grids[0] + grids[1] <= INT32_MAX;
+                    parts[0].waves == parts[1].waves && parts[0].tile == parts[1].tile &&
+                    grids[0] + grids[1] <= INT32_MAX;
   if (grids[0]) launch(0, both);
   if (grids[1] && !both) launch(1, false);
   if (!plan.direct) {
