@@ -51,6 +51,7 @@ struct List {
   float target;  // own tokens: pieces wanted in all; 0 for one piece a sequence
   int piece;     // prefix: tokens of a piece
   int joined;    // own tokens: their rows have prefix pieces too
+  int finish;    // own tokens in one piece: its workgroup adds that many prefix pieces and writes out
   float *opart;
   float2 *ml;
   int2 *where;   // own tokens: first slot and pieces of a sequence that has any
@@ -604,6 +605,65 @@ __device__ __forceinline__ void probabilities(f4 (*s)[2], Rows<HD, NT, F32> &x, 
   for (int n = 0; n < NT; ++n) x.l[n] += sum[n];
 }
 
+// Rows r0 .. r0 + n - 1 (n <= 16) of a sequence whose own sums are in LDS: row i's channels at
+// own[i (HD + 4)], its maximum and sum in m[i] and l[i]. Adds the prefix's pieces and writes out:
+// HD / 4 lanes take four channels each, and groups of such lanes share a row's pieces.
+template <int HD, bool F32, int W>
+__device__ __forceinline__ void finish_rows(const Attn &p, const Job &j, int h, int r0, int n, float S_v,
+                                            float *own, const float *m, const float *l) {
+  constexpr int LANES = HD / 4, GROUPS = 64 * W / LANES, OROW = HD + 4;
+  f4 *so = reinterpret_cast<f4 *>(own + 16 * OROW);  // [GROUPS][LANES], behind the own sums
+  float *sml = own + 16 * OROW + GROUPS * HD;        // [GROUPS][2]
+  const List &k0 = p.list[0].prefix ? p.list[0] : p.list[1];
+  const int slots = k0.slots, g = threadIdx.x / LANES, c = threadIdx.x % LANES;
+  int per = GROUPS;
+  while (per > 1 && per * n > GROUPS) per >>= 1;
+  const int64_t rows = (int64_t)p.tokens * p.group, step = rows * p.kv_heads;
+  for (int i0 = 0; i0 < n; i0 += GROUPS / per) {
+    const int i = i0 + g / per, sub = g & (per - 1);
+    const bool here = i < n, in = here && 4 * c < p.hd;
+    const int64_t at = h * rows + (int64_t)j.q0 * p.group + r0 + i;
+    float M = -INFINITY, L = 0.0f;
+    f4 y = {0, 0, 0, 0};
+    if (here && sub == 0) {
+      M = m[i], L = l[i];
+      if (in) y = *reinterpret_cast<const f4 *>(own + i * OROW + 4 * c);
+    }
+#pragma unroll 4
+    for (int k = sub; k < (here ? slots : 0); k += per) {
+      const float2 ml = k0.ml[at + k * step];
+      f4 o = {0, 0, 0, 0};
+      if (in) o = *reinterpret_cast<const f4 *>(k0.opart + (at + k * step) * p.hd + 4 * c);
+      if (ml.y > 0.0f) {
+        const float to = fmaxf(M, ml.x);
+        const float a = __builtin_amdgcn_exp2f(M - to), e = __builtin_amdgcn_exp2f(ml.x - to);
+        M = to;
+        L = L * a + ml.y * e;
+        y = y * a + o * e;
+      }
+    }
+    if (c == 0) sml[2 * g] = M, sml[2 * g + 1] = L;
+    so[g * LANES + c] = y;
+    __syncthreads();
+    if (here && sub == 0) {
+      for (int k = 1; k < per; ++k) M = fmaxf(M, sml[2 * (g + k)]);
+      L = 0.0f;
+      y = (f4){0, 0, 0, 0};
+      for (int k = 0; k < per; ++k) {
+        if (!(sml[2 * (g + k) + 1] > 0.0f)) continue;
+        const float e = __builtin_amdgcn_exp2f(sml[2 * (g + k)] - M);
+        L += sml[2 * (g + k) + 1] * e;
+        y += so[(g + k) * LANES + c] * e;
+      }
+      const int r = r0 + i, tok = r / p.group, head = h * p.group + (r - tok * p.group);
+      const int64_t to = (int64_t)(j.q0 + tok) * p.heads + head;
+      if (in) store4<F32>(p.out, to * p.hd + 4 * c, y * (L > 0.0f ? S_v / L : 0.0f));
+      if (c == 0 && p.lse) p.lse[to] = L > 0.0f ? kLn2 * (M + __builtin_amdgcn_logf(L)) : -INFINITY;
+    }
+    __syncthreads();
+  }
+}
+
 // W waves take the 32-token tiles of a piece in turn, each for the same 16 NT query rows, and
 // join their sums at the end.
 template <int HD, int NT, bool F32, bool EXACT, int W>
@@ -731,8 +791,9 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
     __syncthreads();
     // 4 W lanes a row, pairs of channels
     const int row = threadIdx.x / (4 * W), col = threadIdx.x % (4 * W), r = r0 + 16 * n + row;
+    const bool finish = NT == 1 && p.list[sh.list].finish > 0;
+    float mm = -INFINITY, ll = 0.0f;
     if (r < rows) {
-      float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
       for (int k = 0; k < W; ++k) mm = fmaxf(mm, sm_m[k][16 * n + row]);
 #pragma unroll
@@ -744,24 +805,26 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
       const int64_t at = (int64_t)(j.q0 + tok) * p.heads + head;
       const float f = sh.direct ? (ll > 0.0f ? S_v / ll : 0.0f) : 1.0f;
       for (int d = 2 * col; d < p.hd; d += 8 * W) {
-        float2 y = make_float2(0.0f, 0.0f);
+        f2 y = {0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < W; ++k) {
-          const f2 z = *reinterpret_cast<const f2 *>(smem + (k * 16 + row) * OROW + d);
-          y.x += z[0], y.y += z[1];
-        }
-        if (sh.direct)
-          store_out<F32>(p.out, at * p.hd + d, y.x * f, y.y * f);
-        else
-          *reinterpret_cast<float2 *>(p.list[sh.list].opart + (part + r) * p.hd + d) = y;
+        for (int k = 0; k < W; ++k) y += *reinterpret_cast<const f2 *>(smem + (k * 16 + row) * OROW + d);
+        if (finish) *reinterpret_cast<f2 *>(smem + row * OROW + d) = y;  // read by this lane alone
+        else if (sh.direct) store_out<F32>(p.out, at * p.hd + d, y[0] * f, y[1] * f);
+        else *reinterpret_cast<f2 *>(p.list[sh.list].opart + (part + r) * p.hd + d) = y;
       }
-      if (col == 0) {
+      if (col == 0 && !finish) {
         if (sh.direct) {
           if (p.lse) p.lse[at] = ll > 0.0f ? kLn2 * (mm - kBase + __builtin_amdgcn_logf(ll)) : -INFINITY;
         } else {
           p.list[sh.list].ml[part + r] = make_float2(mm - kBase, ll);
         }
       }
+    }
+    if (finish) {
+      __syncthreads();  // sm_m and sm_l have been read
+      if (col == 0) sm_m[0][row] = mm - kBase, sm_l[0][row] = ll;
+      __syncthreads();
+      finish_rows<HD, F32, W>(p, j, h, r0, min(16, rows - r0), S_v, smem, sm_m[0], sm_l[0]);
     }
   }
 }
@@ -1023,7 +1086,8 @@ struct Part {      // one launch: the prefix or the sequences' own tokens
 
 struct Plan {
   Part prefix, own;
-  int direct;
+  int direct;  // no partial sums
+  int finish;  // the own tokens' workgroups add the prefix's pieces: no join
 };
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1102,7 +1166,7 @@ Plan plan_of(const KvAttention &a) {
       const int64_t n = a.batch * units, most = n / 20 < 3 ? 3 : n / 20 > 12 ? 12 : n / 20;
       const int w = n <= 256 ? 16 : n <= 512 ? 8 : 4;
       whole = a.max_kv <= 32 * w * most;
-      if (whole) r.waves = w;
+      if (whole) r.waves = w, p.finish = p.prefix.slots > 0;
     }
     // many rows: a row's partial sums cost more than a workgroup's wait, so only where there
     // are far fewer workgroups than the chip holds
@@ -1163,7 +1227,7 @@ int64_t prefix_rows(const KvAttention &a, const Plan &p) {
 }
 int64_t own_rows(const KvAttention &a, const Plan &p) {
   if (p.own.target > 0.0f) return (int64_t)p.own.slots * a.max_q * a.heads;
-  return p.own.slots ? a.tokens * a.heads : 0;
+  return p.own.slots && !p.finish ? a.tokens * a.heads : 0;
 }
 
 template <int HD>
@@ -1216,11 +1280,11 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
   x.piece = plan.prefix.piece, x.opart = opart, x.ml = ml;
   y.table = a.block_table, y.table_width = a.table_width, y.max_len = (int)a.max_kv;
   y.causal = a.causal, y.target = plan.own.target, y.joined = plan.prefix.slots > 0;
-  y.opart = own, y.ml = ml_own, y.where = where;
+  y.opart = own, y.ml = ml_own, y.where = where, y.finish = plan.finish;
   for (int k = 0; k < 2; ++k)
     lists[k].row_tiles = parts[k].row_tiles, lists[k].slots = parts[k].slots;
   const auto launch = [&](int k, bool both) {
-    p.list[0] = lists[k], p.list[1] = lists[1];
+    p.list[0] = lists[k], p.list[1] = lists[!k];
     p.first = (int)grids[k];
     const unsigned g = (unsigned)(grids[k] + (both ? grids[1] : 0));
     if (f32) launch_hd<true>(p, parts[k], g, st);
@@ -1231,7 +1295,7 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
                     grids[0] + grids[1] <= INT32_MAX;
   if (grids[0]) launch(0, both);
   if (grids[1] && !both) launch(1, false);
-  if (!plan.direct) {
+  if (!plan.direct && !plan.finish) {
     Join x = {};
     x.opart = opart, x.opart_own = own, x.ml = ml, x.ml_own = ml_own;
     x.S_v = c.S_v, x.out = a.out, x.lse = a.lse, x.q_offsets = a.q_offsets, x.kv_lens = a.kv_lens;
