@@ -293,8 +293,10 @@ __device__ __forceinline__ unsigned lane_offset(unsigned o) {
 
 // Loads the group at t of page `id`; returns whether the page is one of the cache's. A group
 // that is not there is read from page 0 and never used.
+// (`part` 1: keys only, 2: values only.)
 template <int HD, bool EXACT>
-__device__ __forceinline__ int load_group(const Attn &p, int id, int h, int t, int lane, Group<HD> &x) {
+__device__ __forceinline__ int load_group(const Attn &p, int id, int h, int t, int lane, Group<HD> &x,
+                                          int part = 3) {
   // uniform base addresses and unsigned lane offsets
   const unsigned i = lane & 15, quad = lane >> 4, l = lane;
   const unsigned nb = EXACT ? HD / 16 : (unsigned)p.hd >> 4;  // blocks of a row
@@ -304,51 +306,63 @@ __device__ __forceinline__ int load_group(const Attn &p, int id, int h, int t, i
   typedef const GLOBAL uint8_t *Bytes;
   Bytes kc = (Bytes)(p.kc + row * (nb * 8)), ks = (Bytes)(p.ks + row * nb);
   Bytes vc = (Bytes)(p.vc + row * (nb * 8)), vs = (Bytes)(p.vs + row * nb);
-  if (EXACT) {
-    const unsigned ko = lane_offset(i * (nb * 8) + quad * (HD / 8));
-    if constexpr (HD == 64) {
-      const u2 a = *(const GLOBAL u2 *)(kc + ko);
-      x.k[0] = a.x, x.k[1] = a.y;
+  const unsigned kq = HD == 64 ? 0 : HD == 128 ? quad & 2 : quad * 4;
+  const unsigned vq = HD == 64 ? 0 : HD == 128 ? l & 2 : (l & 3) * 4;
+  if (part & 1) {
+    if (EXACT) {
+      const unsigned ko = lane_offset(i * (nb * 8) + quad * (HD / 8));
+      if constexpr (HD == 64) {
+        const u2 a = *(const GLOBAL u2 *)(kc + ko);
+        x.k[0] = a.x, x.k[1] = a.y;
+      } else {
+#pragma unroll
+        for (int w = 0; w < HD / 128; ++w) {
+          const u4 a = *(const GLOBAL u4 *)(kc + ko + 16 * w);
+          x.k[4 * w] = a.x, x.k[4 * w + 1] = a.y, x.k[4 * w + 2] = a.z, x.k[4 * w + 3] = a.w;
+        }
+      }
+      const unsigned kso = lane_offset(i * nb + (HD == 128 ? kq * 2 : kq));
+      x.ks = *(const GLOBAL unsigned *)(ks + kso);
     } else {
+      x.ks = 0;
 #pragma unroll
-      for (int w = 0; w < HD / 128; ++w) {
-        const u4 a = *(const GLOBAL u4 *)(kc + ko + 16 * w);
-        x.k[4 * w] = a.x, x.k[4 * w + 1] = a.y, x.k[4 * w + 2] = a.z, x.k[4 * w + 3] = a.w;
+      for (unsigned w = 0; w < HD / 64; ++w) {
+        const unsigned b = quad * (HD / 64) + w;
+        u2 a = (u2){0, 0};
+        if (b < nb) {
+          a = *(const GLOBAL u2 *)(kc + (i * nb + b) * 8);
+          x.ks |= (unsigned)ks[i * nb + b] << (8 * w);
+        }
+        x.k[2 * w] = a.x, x.k[2 * w + 1] = a.y;
       }
-    }
-    const unsigned kq = HD == 64 ? 0 : HD == 128 ? quad & 2 : quad * 4;
-    const unsigned vq = HD == 64 ? 0 : HD == 128 ? l & 2 : (l & 3) * 4;
-    const unsigned kso = lane_offset(i * nb + (HD == 128 ? kq * 2 : kq));
-    const unsigned vso = lane_offset((l >> 2) * nb + (HD == 128 ? vq * 2 : vq));
-    x.ks = *(const GLOBAL unsigned *)(ks + kso);
-    x.vs = *(const GLOBAL unsigned *)(vs + vso);
-  } else {
-    x.ks = x.vs = 0;
-#pragma unroll
-    for (unsigned w = 0; w < HD / 64; ++w) {
-      const unsigned b = quad * (HD / 64) + w, c = (l & 3) * (HD / 64) + w;
-      u2 a = (u2){0, 0};
-      if (b < nb) {
-        a = *(const GLOBAL u2 *)(kc + (i * nb + b) * 8);
-        x.ks |= (unsigned)ks[i * nb + b] << (8 * w);
-      }
-      x.k[2 * w] = a.x, x.k[2 * w + 1] = a.y;
-      if (c < nb) x.vs |= (unsigned)vs[(l >> 2) * nb + c] << (8 * w);
     }
   }
-  const bool in = EXACT || (int)(i * (HD / 16)) < p.hd;
-  const unsigned vo = lane_offset(4 * quad * (nb * 8) + i * (HD / 32));
+  if (part & 2) {
+    if (EXACT) {
+      const unsigned vso = lane_offset((l >> 2) * nb + (HD == 128 ? vq * 2 : vq));
+      x.vs = *(const GLOBAL unsigned *)(vs + vso);
+    } else {
+      x.vs = 0;
 #pragma unroll
-  for (unsigned e = 0; e < 4; ++e) {
-    const Bytes v = vc + e * (nb * 8);
-    x.v[e][0] = 0;
-    if constexpr (HD > 128) x.v[e][1] = 0;
-    if (in) {
-      if constexpr (HD == 64) x.v[e][0] = *(const GLOBAL uint16_t *)(v + vo);
-      else if constexpr (HD == 128) x.v[e][0] = *(const GLOBAL unsigned *)(v + vo);
-      else {
-        const u2 a = *(const GLOBAL u2 *)(v + vo);
-        x.v[e][0] = a.x, x.v[e][1] = a.y;
+      for (unsigned w = 0; w < HD / 64; ++w) {
+        const unsigned c = (l & 3) * (HD / 64) + w;
+        if (c < nb) x.vs |= (unsigned)vs[(l >> 2) * nb + c] << (8 * w);
+      }
+    }
+    const bool in = EXACT || (int)(i * (HD / 16)) < p.hd;
+    const unsigned vo = lane_offset(4 * quad * (nb * 8) + i * (HD / 32));
+#pragma unroll
+    for (unsigned e = 0; e < 4; ++e) {
+      const Bytes v = vc + e * (nb * 8);
+      x.v[e][0] = 0;
+      if constexpr (HD > 128) x.v[e][1] = 0;
+      if (in) {
+        if constexpr (HD == 64) x.v[e][0] = *(const GLOBAL uint16_t *)(v + vo);
+        else if constexpr (HD == 128) x.v[e][0] = *(const GLOBAL unsigned *)(v + vo);
+        else {
+          const u2 a = *(const GLOBAL u2 *)(v + vo);
+          x.v[e][0] = a.x, x.v[e][1] = a.y;
+        }
       }
     }
   }
@@ -840,11 +854,14 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
 // alone would take 257 us, the exponentials add about 100, dequantising 60, LDS reads 30.
 template <int HD, int NT, bool F32, bool EXACT, int W>
 __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
-  constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, KS = HD / 32, STAGE = 16 * W;
-  constexpr float kBase = base_of(F32);
-  __shared__ h8 kfrag[2][W][KS][64], vfrag[2][W / 2][DV][64];
-  __shared__ __align__(16) _Float16 vs_lds[W][DV * kVsRow];
-  __shared__ int oks[2][W];
+  // Groups of a stage. At HD 256 LDS holds half as many: of eight waves two take a group, one its
+  // keys, one its values, against four waves on a SIMD each: 2000 x 4000 queries 244 -> 164 us. In
+  // fp32 eight cost 172 us against 152 (2 x 1000 x 3000): four.
+  constexpr int GS = HD > 128 && W > 4 ? W / 2 : W, STAGE = 16 * GS;
+  constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, KS = HD / 32;
+  __shared__ h8 kfrag[2][GS][KS][64], vfrag[2][GS / 2][DV][64];
+  __shared__ __align__(16) _Float16 vs_lds[GS][DV * kVsRow];
+  __shared__ int oks[2][GS];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int i = lane & 15, quad = lane >> 4;
@@ -866,24 +883,29 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   Group<HD> g;
   int ok = 0;
   Pages pg = open_pages(j, p.page_shift, t0, t1, lane);
+  const int mine = wave % GS, part_kv = GS == W ? 3 : 1 + wave / GS;
   const auto fetch = [&](int t) {  // this wave's group of the stage at t
-    t += 16 * wave;
-    ok = load_group<HD, EXACT>(p, page_of(pg, t), h, t, lane, g);
+    t += 16 * mine;
+    ok = load_group<HD, EXACT>(p, page_of(pg, t), h, t, lane, g, part_kv);
   };
   const auto dequantise = [&](int b) {
-    stage_value_scales<HD, EXACT>(g, lane, vs_lds[wave]);
-    if (lane == 0) oks[b][wave] = ok;
-    h8 kf[KS];
-    key_frags<HD, EXACT>(g, lane, kf);
+    if (part_kv & 2) stage_value_scales<HD, EXACT>(g, lane, vs_lds[mine]);
+    if (part_kv & 1) {
+      if (lane == 0) oks[b][mine] = ok;
+      h8 kf[KS];
+      key_frags<HD, EXACT>(g, lane, kf);
 #pragma unroll
-    for (int k = 0; k < KS; ++k) kfrag[b][wave][k][lane] = kf[k];
-    order_wave_lds();
-    h4 vf[DV];
-    value_frags<HD>(g, lane, vs_lds[wave], vf);
+      for (int k = 0; k < KS; ++k) kfrag[b][mine][k][lane] = kf[k];
+    }
+    if (part_kv & 2) {
+      order_wave_lds();
+      h4 vf[DV];
+      value_frags<HD>(g, lane, vs_lds[mine], vf);
 #pragma unroll
-    for (int d = 0; d < DV; ++d)
-      reinterpret_cast<h4 *>(&vfrag[b][wave >> 1][d][lane])[wave & 1] = vf[d];
-    order_wave_lds();
+      for (int d = 0; d < DV; ++d)
+        reinterpret_cast<h4 *>(&vfrag[b][mine >> 1][d][lane])[mine & 1] = vf[d];
+      order_wave_lds();
+    }
   };
   Rows<HD, NT, F32> x;
   {
@@ -904,10 +926,14 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   for (const int te = min(t1, pg.t + kRun); t < te; t += STAGE, b ^= 1) {  // the stages of a run
     // operands are read one step ahead of their products: the values' before the exponentials,
     // the next tile's keys before the second product
-    const int tiles = min(W / 2, (min(t1, lim_hi) - t + 31) >> 5);
-    h8 kf[2 * KS];
+    // (at HD 256 they would not fit beside the sums)
+    constexpr bool AHEAD = HD <= 128;
+    const int tiles = min(GS / 2, (min(t1, lim_hi) - t + 31) >> 5);
+    h8 kf[AHEAD ? 2 * KS : 1];
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[b][k / KS][k % KS][lane];
+      for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[b][k / KS][k % KS][lane];
+    }
 #pragma unroll 1
     for (int c = 0; c < tiles; ++c) {
       const int tt = t + 32 * c;
@@ -918,32 +944,40 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+          const h8 a = AHEAD ? kf[AHEAD ? u * KS + k : 0] : kfrag[b][2 * c + u][k][lane];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int q = 0; q < HALVES; ++q)
-              s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u * KS + k], x.q[n][q][k], s[n][u], 0, 0, 0);
-      h8 vf[DV];
+              s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, x.q[n][q][k], s[n][u], 0, 0, 0);
+        }
+      h8 vf[AHEAD ? DV : 1];
+      if constexpr (AHEAD) {
 #pragma unroll
-      for (int d = 0; d < DV; ++d) vf[d] = vfrag[b][c][d][lane];
+        for (int d = 0; d < DV; ++d) vf[d] = vfrag[b][c][d][lane];
+      }
       const int seen = __builtin_amdgcn_readfirstlane(oks[b][2 * c] | oks[b][2 * c + 1] << 1);
       __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
       if (tt + 32 > lim_lo || seen != 3) hide<NT>(s, x.lim, tt, t1, seen, quad);
       h8 pf[NT][HALVES];
       probabilities<HD, NT, F32>(s, x, pf);
-      const int nc = min(c + 1, W / 2 - 1);
+      if constexpr (AHEAD) {
+        const int nc = min(c + 1, GS / 2 - 1);
 #pragma unroll
-      for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[b][2 * nc + k / KS][k % KS][lane];
-      __builtin_amdgcn_sched_barrier(0);
+        for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[b][2 * nc + k / KS][k % KS][lane];
+        __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
-      for (int d = 0; d < DV; ++d)
+      for (int d = 0; d < DV; ++d) {
+        const h8 a = AHEAD ? vf[AHEAD ? d : 0] : vfrag[b][c][d][lane];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int q = 0; q < HALVES; ++q)
-            x.acc[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], pf[n][q], x.acc[n][d], 0, 0, 0);
+            x.acc[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf[n][q], x.acc[n][d], 0, 0, 0);
+      }
     }
     if (t + STAGE < t1) {
       dequantise(b ^ 1);
@@ -1114,7 +1148,7 @@ Part tile_part(const KvAttention &a, int64_t rows, int64_t jobs, int64_t len) {
   const bool wide = hd > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
   r.tile = 1;
   r.nt = wide || f32 || small || rows <= 64 ? 1 : 2;
-  r.waves = wide || small || rows <= 64 * r.nt ? 4 : 8;
+  r.waves = small || rows <= 64 * r.nt || (wide && f32) ? 4 : 8;
   r.resident = 256 * (wide ? 1 : (hd > 64 || r.waves == 8 ? 8 / r.waves : 3));
   r.row_tiles = (int)cdiv(rows, 16 * r.nt * r.waves);
   return r;
@@ -1185,8 +1219,8 @@ void launch_rows(const Attn &p, const Part &r, unsigned grid, hipStream_t st) {
   const dim3 g(grid), b(64 * r.waves);
   if (r.tile) {
     if (r.waves == 8) {
-      if constexpr (HD <= 128)
-        hipLaunchKernelGGL((k_kv_attn_tile<HD, F32 ? 1 : 2, F32, EXACT, 8>), g, b, 0, st, p);
+      if constexpr (HD <= 128 || !F32)
+        hipLaunchKernelGGL((k_kv_attn_tile<HD, F32 || (HD > 128) ? 1 : 2, F32, EXACT, 8>), g, b, 0, st, p);
     } else if (r.nt == 1) {
       hipLaunchKernelGGL((k_kv_attn_tile<HD, 1, F32, EXACT, 4>), g, b, 0, st, p);
     } else if constexpr (HD <= 128 && !F32) {

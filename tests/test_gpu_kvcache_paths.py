@@ -121,3 +121,18 @@ def test_page_runs_and_pages_larger_than_a_run():
         check(c, attend(c))
         c = ref.make(n, BF, [50], [n], 2, 1, 64, ps, spare_pages=1)
         check(c, attend(c))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("hd", [64, 80, 128, 144, 256])
+@pytest.mark.parametrize("rows", [50, 100, 150, 280])
+def test_large_calls(dtype, hd, rows):
+    """Calls of over 512 workgroups, whose tiles are larger: rows in one, two and more tiles,
+    contexts of unequal lengths, one of them empty; the second call over a prefix alone and own tokens."""
+    case(f"kv attention, {rows} rows a head of {hd}, {dtype}, many workgroups")
+    q = rows // 2
+    lens = [1030, 1030 - q, 0, 517, 130, 1029, 800, 31]
+    c = ref.make(rows + hd, dtype, [q, q - 1, 0, 3, q, 1, q // 2, 31 % (q + 1)], lens, 16, 8, hd, 32)
+    check(c, attend(c))
+    c = ref.make(rows + hd + 1, dtype, [rows // 4, 1, rows // 4 - 1], [rows // 4, 300, 40], 16, 8, hd, 32, 8200)
+    check(c, attend(c))
