@@ -79,14 +79,15 @@ NVFP4_API int nvfp4_kv_read(const nvfp4_kv_cache *cache, const int64_t *slots, i
  *   out[i][j] = sum_t p_t v_t,  p = softmax over the seen tokens of scale * (q[i][j] . k_t);
  *   lse[i][j] (nullable, fp32) = ln sum_t exp(scale * (q[i][j] . k_t)).
  * A row that sees nothing gets out = 0 and lse = -inf. Rows of out and lse that belong to no
- * sequence hold unspecified values. Page ids outside [0, pages) hide the page's tokens; kv_lens is cut
- * to [0, max_kv].
+ * sequence hold unspecified values. Page ids outside [0, pages) hide the page's tokens; kv_lens
+ * is cut to [0, max_kv].
  *
  * Products take fp16 operands (cached values without S are exact in fp16; bf16 queries are
  * scaled by a power of two per row, probabilities are rounded to 11 bits, and to multiples of
  * 2^-31 of the row's largest) with fp32 sums; for fp32 q, queries and probabilities are split
- * in two fp16 halves (22 bits, multiples of 2^-37). Softmax statistics are fp32. out: [tokens][heads][head_dim] contiguous, of `dtype`. Partial sums are joined in
- * a fixed order: results are bitwise reproducible for the same arguments and device.
+ * in two fp16 halves (22 bits, multiples of 2^-37). Softmax statistics are fp32.
+ * out: [tokens][heads][head_dim] contiguous, of `dtype`. Partial sums are joined in a fixed
+ * order: results are bitwise reproducible for the same arguments and device.
  *
  * workspace: 16-byte aligned, at least nvfp4_kv_attention_workspace_size() bytes (may be 0),
  * no initialisation needed; calls that share it must not overlap.
