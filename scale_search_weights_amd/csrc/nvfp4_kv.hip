@@ -1,23 +1,22 @@
 // Key/value cache in NVFP4: quantise rows into cache slots, and read slots back.
 //
-// Both kernels take (token, head) rows of head_dim values, eight values per lane (half a
-// block), so a row is head_dim / 8 lanes and a workgroup of 256 takes 256 / (head_dim / 8) rows
-// of one head at a time: its tensor scale is uniform, and consecutive tokens of a page are
-// contiguous in the cache, so a workgroup's stores join into whole lines. They are bound by
-// memory: write moves 2 or 4 bytes in and 9/16 out per value, read the reverse. 131072 tokens of
-// 8 heads of 128 are read in 137 us, 5.0 TB/s, what a 1 GiB copy reaches; 16384 tokens are
-// written and read in 38 us, 4.5 TB/s. Values that are read back are stored non-temporally (143 us
-// with ordinary stores); codes are not, the attention that follows finds them in the caches.
+// Both kernels take (token, head) rows of head_dim values, one head to a workgroup: its tensor
+// scale is uniform, and consecutive tokens of a page are contiguous in the cache, so a
+// workgroup's stores join into whole lines. A lane of write takes a block of 16: its maximum
+// needs no exchange, and the fp64 work on its scale, which costs as much as its values, is done
+// once (with half a block a lane 16384 tokens of 8 heads of 128 took 4 us more). A lane of read
+// takes the values of 16 bytes of output, so the lanes of a store are contiguous.
+//
+// They are bound by memory: write moves 2 or 4 bytes in and 9/16 out per value, read the reverse.
+// 131072 tokens of 8 heads of 128 are read in 137 us, 5.0 TB/s, what a 1 GiB copy reaches; 16384
+// tokens are written and read in 34 us, 5.0 TB/s; 30000 in fp32 in 116 us, 4.8 TB/s (190 us with
+// eight values a lane of read, two strided stores). Values that are read back are stored
+// non-temporally (143 us with ordinary stores); codes are not, the attention that follows finds
+// them in the caches.
 #include "nvfp4_device.h"
 #include "nvfp4_kv.h"
 
 namespace nvfp4 {
-
-// maximum with the other lane of a pair (lanes 2i, 2i + 1)
-__device__ __forceinline__ float pair_max(float x) {
-  const int o = __builtin_amdgcn_mov_dpp(__float_as_int(x), 0xB1, 0xF, 0xF, true);
-  return fmaxf(x, __int_as_float(o));
-}
 
 template <int DT>
 __device__ __forceinline__ void load8(const void *x, int64_t e, float v[8]) {
@@ -35,11 +34,13 @@ __device__ __forceinline__ void load8(const void *x, int64_t e, float v[8]) {
 
 // Rows a lane takes at once, their loads issued together: without it a wave waits for one row's
 // slot and then its codes, and read ran at 3.5 TB/s (131072 tokens, 8 heads of 128: 200 us;
-// with 4 rows 143 us, 2 or 8 rows 3 to 8% slower). Below 128 Ki lanes a row one row a lane is
-// faster (48 tokens written and read: 5.4 us, 7.3 us with 4).
-constexpr int kRowsALane = 4;
+// with 4 rows 143 us, 2 or 8 rows 3 to 8% slower). Write: 16384 tokens written and read 35.4 us
+// with 1 row, 34.2 with 2, 35.6 with 4. Calls of fewer values than kFewValues fill the chip with
+// one row a lane only (48 tokens written and read: 5.4 us, 7.3 us with 4).
+constexpr int kReadRows = 4, kWriteRows = 2;
+constexpr int64_t kFewValues = 4 << 20;
 
-// Slots of this lane's U rows: rows are dealt U x 256 / lanes to a workgroup; -1 past the end
+// Slots of this lane's U rows: a workgroup takes U x 256 / lanes; -1 past the end
 // and for tokens without a slot in the cache.
 template <int U>
 __device__ __forceinline__ void load_slots(const int64_t *slots, int64_t n, int64_t n_slots,
@@ -63,9 +64,9 @@ struct KvWrite {
 template <int DT, int U>
 __global__ void __launch_bounds__(256) k_kv_write(KvWrite p) {
   const int kv = blockIdx.z, h = blockIdx.y;
-  const int lanes = p.head_dim >> 3, rows = 256 / lanes;
+  const int lanes = p.head_dim >> 4, rows = 256 / lanes;
   const int row = threadIdx.x / lanes, part = threadIdx.x - row * lanes;
-  if (row >= rows) return;  // whole lane pairs: lanes is even
+  if (row >= rows) return;
   const float S = p.S[kv][h];
   float lo6, hi6;
   recip_bracket(6.0 * (double)S, lo6, hi6);
@@ -73,45 +74,45 @@ __global__ void __launch_bounds__(256) k_kv_write(KvWrite p) {
   const int64_t step = (int64_t)U * rows;
   for (int64_t t = blockIdx.x * step + row; t < p.tokens; t += gridDim.x * step) {
     int64_t slot[U];
-    float v[U][8];
+    float v[U][16];
 #pragma unroll
-    for (int u = 0; u < U; ++u)  // loads of all rows first, also of tokens that are skipped
-      load8<DT>(p.x[kv], min(t + u * rows, p.tokens - 1) * p.ts[kv] + h * p.hs[kv] + part * 8, v[u]);
+    for (int u = 0; u < U; ++u) {  // loads of all rows first, also of tokens that are skipped
+      const int64_t e = min(t + u * rows, p.tokens - 1) * p.ts[kv] + h * p.hs[kv] + part * 16;
+      load8<DT>(p.x[kv], e, v[u]);
+      load8<DT>(p.x[kv], e + 8, v[u] + 8);
+    }
     load_slots<U>(p.slots, p.tokens, p.n_slots, t, rows, slot);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (slot[u] < 0) continue;  // the same for the whole row
+      if (slot[u] < 0) continue;
       float amax = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[u][i]));
-      amax = pair_max(amax);
+      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[u][i]));
       const int b = max_scale_byte_fast(amax, lo6, hi6, S);
-      unsigned c = 0u;
+      uint2 c = {0u, 0u};
       if (b) {
         const double sS = e4m3_value_d(b) * (double)S;
         float lo, hi;
         recip_bracket(sS, lo, hi);
-        c = fp4_clear_neg_zero(fp4_exact_codes8(v[u], lo, hi, sS));
+        c.x = fp4_clear_neg_zero(fp4_exact_codes8(v[u], lo, hi, sS));
+        c.y = fp4_clear_neg_zero(fp4_exact_codes8(v[u] + 8, lo, hi, sS));
       }
       const int64_t at = (((slot[u] >> p.page_shift) * p.heads + h) << p.page_shift) + (slot[u] & mask);
-      reinterpret_cast<unsigned *>(p.codes[kv])[at * lanes + part] = c;
-      if (!(part & 1)) p.scales[kv][at * (lanes >> 1) + (part >> 1)] = (uint8_t)b;
+      reinterpret_cast<uint2 *>(p.codes[kv])[at * lanes + part] = c;
+      p.scales[kv][at * lanes + part] = (uint8_t)b;
     }
   }
 }
 
 static int page_shift_of(const nvfp4_kv_cache &c) { return __builtin_ctzll((unsigned long long)c.page_size); }
 
-static dim3 row_grid(int64_t tokens, int64_t heads, int64_t head_dim, int z, int u) {
-  const int64_t rows = 256 / (head_dim / 8) * u;
+// Grid for `tokens` rows of `lanes` lanes, u rows a lane.
+static dim3 row_grid(int64_t tokens, int64_t heads, int64_t lanes, int z, int u) {
+  const int64_t rows = 256 / lanes * u;
   int64_t g = (tokens + rows - 1) / rows;
   int64_t cap = 65536 / (heads * z);  // rows beyond are taken in a loop
   if (cap < 64) cap = 64;
   return dim3((unsigned)(g < cap ? g : cap), (unsigned)heads, (unsigned)z);
-}
-
-static int rows_a_lane(int64_t tokens, int64_t heads, int64_t head_dim, int z) {
-  return tokens * heads * z * (head_dim / 8) < 128 * 1024 * kRowsALane ? 1 : kRowsALane;
 }
 
 int launch_kv_write(const nvfp4_kv_cache &c, const void *k, const void *v, int dtype,
@@ -125,14 +126,14 @@ int launch_kv_write(const nvfp4_kv_cache &c, const void *k, const void *v, int d
   p.S[0] = c.S_k, p.S[1] = c.S_v;
   p.slots = slots, p.tokens = tokens, p.n_slots = c.pages * c.page_size;
   p.heads = (int)c.kv_heads, p.head_dim = (int)c.head_dim, p.page_shift = page_shift_of(c);
-  const int u = rows_a_lane(tokens, c.kv_heads, c.head_dim, 2);
-  const dim3 g = row_grid(tokens, c.kv_heads, c.head_dim, 2, u), b(256);
+  const int u = tokens * c.kv_heads * c.head_dim * 2 < kFewValues ? 1 : kWriteRows;
+  const dim3 g = row_grid(tokens, c.kv_heads, c.head_dim / 16, 2, u), b(256);
   if (dtype == NVFP4_DTYPE_BF16) {
     if (u == 1) hipLaunchKernelGGL((k_kv_write<NVFP4_DTYPE_BF16, 1>), g, b, 0, st, p);
-    else hipLaunchKernelGGL((k_kv_write<NVFP4_DTYPE_BF16, kRowsALane>), g, b, 0, st, p);
+    else hipLaunchKernelGGL((k_kv_write<NVFP4_DTYPE_BF16, kWriteRows>), g, b, 0, st, p);
   } else {
     if (u == 1) hipLaunchKernelGGL((k_kv_write<NVFP4_DTYPE_F32, 1>), g, b, 0, st, p);
-    else hipLaunchKernelGGL((k_kv_write<NVFP4_DTYPE_F32, kRowsALane>), g, b, 0, st, p);
+    else hipLaunchKernelGGL((k_kv_write<NVFP4_DTYPE_F32, kWriteRows>), g, b, 0, st, p);
   }
   return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
@@ -149,10 +150,14 @@ struct KvRead {
 typedef unsigned kv_u4 __attribute__((ext_vector_type(4)));
 typedef float kv_f4 __attribute__((ext_vector_type(4)));
 
+// Values a lane of read takes: 16 bytes of output, so that the lanes of a store are contiguous.
+constexpr int read_values(int dt) { return dt == NVFP4_DTYPE_BF16 ? 8 : 4; }
+
 template <int DT, int U>
 __global__ void __launch_bounds__(256) k_kv_read(KvRead p) {
+  constexpr int V = read_values(DT);
   const int kv = blockIdx.z, h = blockIdx.y;
-  const int lanes = p.head_dim >> 3, rows = 256 / lanes;
+  const int lanes = p.head_dim / V, rows = 256 / lanes;
   const int row = threadIdx.x / lanes, part = threadIdx.x - row * lanes;
   if (row >= rows) return;
   const float S = p.S[kv][h];
@@ -167,8 +172,9 @@ __global__ void __launch_bounds__(256) k_kv_read(KvRead p) {
       c[u] = b[u] = 0u;  // no slot: zeros
       if (slot[u] >= 0) {
         const int64_t at = (((slot[u] >> p.page_shift) * p.heads + h) << p.page_shift) + (slot[u] & mask);
-        c[u] = reinterpret_cast<const unsigned *>(p.codes[kv])[at * lanes + part];
-        b[u] = p.scales[kv][at * (lanes >> 1) + (part >> 1)];
+        if (V == 8) c[u] = reinterpret_cast<const unsigned *>(p.codes[kv])[at * lanes + part];
+        else c[u] = reinterpret_cast<const uint16_t *>(p.codes[kv])[at * lanes + part];
+        b[u] = p.scales[kv][at * (lanes * V / 16) + part * V / 16];
       }
     }
 #pragma unroll
@@ -178,17 +184,15 @@ __global__ void __launch_bounds__(256) k_kv_read(KvRead p) {
       float y[8];
       fp4_decode8(c[u], y);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = y[i] * s * S;  // g s is exact
-      const int64_t e = ((t + u * rows) * p.heads + h) * p.head_dim + part * 8;
+      for (int i = 0; i < V; ++i) y[i] = y[i] * s * S;  // g s is exact
+      const int64_t e = ((t + u * rows) * p.heads + h) * p.head_dim + part * V;
       if (DT == NVFP4_DTYPE_BF16) {
         const kv_u4 w = {bf16x2_bits(y[0], y[1]), bf16x2_bits(y[2], y[3]), bf16x2_bits(y[4], y[5]),
                          bf16x2_bits(y[6], y[7])};
         __builtin_nontemporal_store(w, reinterpret_cast<kv_u4 *>(static_cast<uint16_t *>(p.y[kv]) + e));
       } else {
-        kv_f4 *o = reinterpret_cast<kv_f4 *>(static_cast<float *>(p.y[kv]) + e);
-        const kv_f4 w0 = {y[0], y[1], y[2], y[3]}, w1 = {y[4], y[5], y[6], y[7]};
-        __builtin_nontemporal_store(w0, o);
-        __builtin_nontemporal_store(w1, o + 1);
+        const kv_f4 w = {y[0], y[1], y[2], y[3]};
+        __builtin_nontemporal_store(w, reinterpret_cast<kv_f4 *>(static_cast<float *>(p.y[kv]) + e));
       }
     }
   }
@@ -203,14 +207,14 @@ int launch_kv_read(const nvfp4_kv_cache &c, const int64_t *slots, int64_t n, voi
   if (z == 0) return NVFP4_OK;
   p.slots = slots, p.n = n, p.n_slots = c.pages * c.page_size;
   p.heads = (int)c.kv_heads, p.head_dim = (int)c.head_dim, p.page_shift = page_shift_of(c);
-  const int u = rows_a_lane(n, c.kv_heads, c.head_dim, z);
-  const dim3 g = row_grid(n, c.kv_heads, c.head_dim, z, u), b(256);
+  const int u = n * c.kv_heads * c.head_dim * z < kFewValues ? 1 : kReadRows;
+  const dim3 g = row_grid(n, c.kv_heads, c.head_dim / read_values(out_dtype), z, u), b(256);
   if (out_dtype == NVFP4_DTYPE_BF16) {
     if (u == 1) hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_BF16, 1>), g, b, 0, st, p);
-    else hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_BF16, kRowsALane>), g, b, 0, st, p);
+    else hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_BF16, kReadRows>), g, b, 0, st, p);
   } else {
     if (u == 1) hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_F32, 1>), g, b, 0, st, p);
-    else hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_F32, kRowsALane>), g, b, 0, st, p);
+    else hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_F32, kReadRows>), g, b, 0, st, p);
   }
   return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }

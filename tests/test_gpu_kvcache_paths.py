@@ -9,6 +9,7 @@ import torch
 import kvcache_ref as ref
 from scale_search_weights_amd import kvcache
 from test_gpu_kvcache import BF, DEV, F32, attend, case, check, on_gpu, strided
+from test_gpu_kvcache import test_write_matches_the_quantiser_and_read_dequantises as write_and_read
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +137,10 @@ def test_large_calls(dtype, hd, rows):
     check(c, attend(c))
     c = ref.make(rows + hd + 1, dtype, [rows // 4, 1, rows // 4 - 1], [rows // 4, 300, 40], 16, 8, hd, 32, 8200)
     check(c, attend(c))
+
+
+@pytest.mark.parametrize("dtype,tokens,heads,hd,page_size", [
+    (BF, 4999, 4, 112, 32), (F32, 4999, 4, 112, 32),        # several rows a lane, an odd count of tokens
+    (BF, 40003, 4, 16, 16), (F32, 2051, 1, 1024, 64)])      # the smallest and the largest rows
+def test_write_and_read_of_many_tokens(dtype, tokens, heads, hd, page_size):
+    write_and_read(dtype, tokens, heads, hd, page_size, None, False)
