@@ -8,11 +8,12 @@
 // takes the values of 16 bytes of output, so the lanes of a store are contiguous.
 //
 // They are bound by memory: write moves 2 or 4 bytes in and 9/16 out per value, read the reverse.
-// 131072 tokens of 8 heads of 128 are read in 137 us, 5.0 TB/s, what a 1 GiB copy reaches; 16384
-// tokens are written and read in 34 us, 5.0 TB/s; 30000 in fp32 in 116 us, 4.8 TB/s (190 us with
-// eight values a lane of read, two strided stores). Values that are read back are stored
-// non-temporally (143 us with ordinary stores); codes are not, the attention that follows finds
-// them in the caches.
+// 131072 tokens of 8 heads of 128 are read in 134 us, 5.1 TB/s, what a 1 GiB copy reaches; 16384
+// tokens are written and read in 34 us, 5.0 TB/s; 30000 in fp32 in 99 us, 5.7 TB/s (eight
+// values a lane of read, two strided stores, cost 74 us more). Values that are read back are stored
+// non-temporally (134 us, 143 with ordinary stores), except in rows of no whole 64 bytes (19103
+// tokens of 11 heads of 112: 20 us, 28 non-temporally); codes are not, the attention that follows
+// finds them in the caches.
 #include "nvfp4_device.h"
 #include "nvfp4_kv.h"
 
@@ -51,6 +52,22 @@ __device__ __forceinline__ void load_slots(const int64_t *slots, int64_t n, int6
   for (int u = 0; u < U; ++u) slot[u] = slot[u] < n_slots ? slot[u] : -1;
 }
 
+// The (head, first token, token step) of a workgroup. Large calls (DIES): workgroups go to the 8
+// dies in turn, and those of one chunk of tokens follow each other on one die, so that lines shared
+// by neighbouring heads meet in its L2. (With heads far apart in the grid: rows of 160 bytes, 101071
+// tokens of 12 heads, 213 us read, 131 so; rows of 512, 30000 tokens written and read, 116 and 99.
+// In small calls that order costs 0.3 to 1 us.)
+struct Place {
+  int h;
+  int64_t t, step;
+};
+template <bool DIES>
+__device__ __forceinline__ Place place_of(int heads, int per) {
+  if (!DIES) return {(int)blockIdx.z, (int64_t)blockIdx.x * per, (int64_t)gridDim.x * per};
+  const int die = blockIdx.x & 7, j = blockIdx.x >> 3, chunk = j / heads;
+  return {j - chunk * heads, (int64_t)(chunk * 8 + die) * per, (int64_t)(gridDim.x / heads) * per};
+}
+
 struct KvWrite {
   const void *x[2];
   int64_t ts[2], hs[2];
@@ -63,16 +80,16 @@ struct KvWrite {
 
 template <int DT, int U>
 __global__ void __launch_bounds__(256) k_kv_write(KvWrite p) {
-  const int kv = blockIdx.z, h = blockIdx.y;
   const int lanes = p.head_dim >> 4, rows = 256 / lanes;
+  const Place at0 = place_of<(U > 1)>(p.heads, U * rows);
+  const int kv = blockIdx.y, h = at0.h;
   const int row = threadIdx.x / lanes, part = threadIdx.x - row * lanes;
   if (row >= rows) return;
   const float S = p.S[kv][h];
   float lo6, hi6;
   recip_bracket(6.0 * (double)S, lo6, hi6);
   const int64_t mask = ((int64_t)1 << p.page_shift) - 1;
-  const int64_t step = (int64_t)U * rows;
-  for (int64_t t = blockIdx.x * step + row; t < p.tokens; t += gridDim.x * step) {
+  for (int64_t t = at0.t + row; t < p.tokens; t += at0.step) {
     int64_t slot[U];
     float v[U][16];
 #pragma unroll
@@ -106,13 +123,14 @@ __global__ void __launch_bounds__(256) k_kv_write(KvWrite p) {
 
 static int page_shift_of(const nvfp4_kv_cache &c) { return __builtin_ctzll((unsigned long long)c.page_size); }
 
-// Grid for `tokens` rows of `lanes` lanes, u rows a lane.
+// Grid for `tokens` rows of `lanes` lanes, u rows a lane, as place_of reads it.
 static dim3 row_grid(int64_t tokens, int64_t heads, int64_t lanes, int z, int u) {
   const int64_t rows = 256 / lanes * u;
-  int64_t g = (tokens + rows - 1) / rows;
-  int64_t cap = 65536 / (heads * z);  // rows beyond are taken in a loop
+  int64_t g = (tokens + rows - 1) / rows, cap = 65536 / (heads * z);  // the rest in a loop
   if (cap < 64) cap = 64;
-  return dim3((unsigned)(g < cap ? g : cap), (unsigned)heads, (unsigned)z);
+  if (g > cap) g = cap;
+  if (u == 1) return dim3((unsigned)g, (unsigned)z, (unsigned)heads);
+  return dim3((unsigned)((g + 7) / 8 * 8 * heads), (unsigned)z);
 }
 
 int launch_kv_write(const nvfp4_kv_cache &c, const void *k, const void *v, int dtype,
@@ -153,17 +171,17 @@ typedef float kv_f4 __attribute__((ext_vector_type(4)));
 // Values a lane of read takes: 16 bytes of output, so that the lanes of a store are contiguous.
 constexpr int read_values(int dt) { return dt == NVFP4_DTYPE_BF16 ? 8 : 4; }
 
-template <int DT, int U>
+template <int DT, int U, bool STREAM>  // STREAM: rows are whole pieces of 64 bytes
 __global__ void __launch_bounds__(256) k_kv_read(KvRead p) {
   constexpr int V = read_values(DT);
-  const int kv = blockIdx.z, h = blockIdx.y;
   const int lanes = p.head_dim / V, rows = 256 / lanes;
+  const Place at0 = place_of<(U > 1)>(p.heads, U * rows);
+  const int kv = blockIdx.y, h = at0.h;
   const int row = threadIdx.x / lanes, part = threadIdx.x - row * lanes;
   if (row >= rows) return;
   const float S = p.S[kv][h];
   const int64_t mask = ((int64_t)1 << p.page_shift) - 1;
-  const int64_t step = (int64_t)U * rows;
-  for (int64_t t = blockIdx.x * step + row; t < p.n; t += gridDim.x * step) {
+  for (int64_t t = at0.t + row; t < p.n; t += at0.step) {
     int64_t slot[U];
     unsigned c[U], b[U];
     load_slots<U>(p.slots, p.n, p.n_slots, t, rows, slot);
@@ -189,7 +207,9 @@ __global__ void __launch_bounds__(256) k_kv_read(KvRead p) {
       if (DT == NVFP4_DTYPE_BF16) {
         const kv_u4 w = {bf16x2_bits(y[0], y[1]), bf16x2_bits(y[2], y[3]), bf16x2_bits(y[4], y[5]),
                          bf16x2_bits(y[6], y[7])};
-        __builtin_nontemporal_store(w, reinterpret_cast<kv_u4 *>(static_cast<uint16_t *>(p.y[kv]) + e));
+        kv_u4 *o = reinterpret_cast<kv_u4 *>(static_cast<uint16_t *>(p.y[kv]) + e);
+        if (STREAM) __builtin_nontemporal_store(w, o);
+        else *o = w;  // the caches join the pieces
       } else {
         const kv_f4 w = {y[0], y[1], y[2], y[3]};
         __builtin_nontemporal_store(w, reinterpret_cast<kv_f4 *>(static_cast<float *>(p.y[kv]) + e));
@@ -209,12 +229,15 @@ int launch_kv_read(const nvfp4_kv_cache &c, const int64_t *slots, int64_t n, voi
   p.heads = (int)c.kv_heads, p.head_dim = (int)c.head_dim, p.page_shift = page_shift_of(c);
   const int u = n * c.kv_heads * c.head_dim * z < kFewValues ? 1 : kReadRows;
   const dim3 g = row_grid(n, c.kv_heads, c.head_dim / read_values(out_dtype), z, u), b(256);
-  if (out_dtype == NVFP4_DTYPE_BF16) {
-    if (u == 1) hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_BF16, 1>), g, b, 0, st, p);
-    else hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_BF16, kReadRows>), g, b, 0, st, p);
+  if (out_dtype == NVFP4_DTYPE_F32) {
+    if (u == 1) hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_F32, 1, true>), g, b, 0, st, p);
+    else hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_F32, kReadRows, true>), g, b, 0, st, p);
+  } else if (u == 1) {  // small: what is stored stays in the caches either way
+    hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_BF16, 1, false>), g, b, 0, st, p);
+  } else if (c.head_dim % 32) {
+    hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_BF16, kReadRows, false>), g, b, 0, st, p);
   } else {
-    if (u == 1) hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_F32, 1>), g, b, 0, st, p);
-    else hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_F32, kReadRows>), g, b, 0, st, p);
+    hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_BF16, kReadRows, true>), g, b, 0, st, p);
   }
   return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
