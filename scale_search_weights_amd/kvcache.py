@@ -97,6 +97,14 @@ class KVCache:
 
 _BF16, _F32, _I32, _INT64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream without a Stream object
+_current_device = torch._C._cuda_getDevice
+
+
+def _stream(cache: KVCache) -> int:
+    """The current stream; the cache's GPU has to be the current one, where kernels are launched."""
+    if _current_device() != cache._index:
+        raise ValueError(f"the cache is on {cache.device}, the current device is cuda:{_current_device()}")
+    return _raw_stream(cache._index)
 
 
 def _rows(t, name: str, cache: KVCache, heads: int | None):
@@ -145,8 +153,9 @@ def write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor)
     _ids(slots, "slots", cache, 1, _INT64)
     if slots.shape[0] != n:
         raise ValueError(f"slots must have {n} elements, got {slots.shape[0]}")
-    _check((_bound or lib()).nvfp4_kv_write(cache._ref, k.data_ptr(), v.data_ptr(), dt, n, k_ts, k_hs,
-                                v_ts, v_hs, slots.data_ptr(), _raw_stream(cache._index)), "nvfp4_kv_write")
+    _check((_bound or lib()).nvfp4_kv_write(
+        cache._ref, k.data_ptr(), v.data_ptr(), dt, n, k_ts, k_hs, v_ts, v_hs, slots.data_ptr(),
+        _stream(cache)), "nvfp4_kv_write")
 
 
 def read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16):
@@ -158,8 +167,8 @@ def read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat1
     n = slots.shape[0]
     k = torch.empty((n, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
     v = torch.empty_like(k)
-    _check((_bound or lib()).nvfp4_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _dt(k),
-                               _raw_stream(cache._index)), "nvfp4_kv_read")
+    _check((_bound or lib()).nvfp4_kv_read(
+        cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _dt(k), _stream(cache)), "nvfp4_kv_read")
     return k, v
 
 
@@ -254,5 +263,5 @@ def attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor | None 
         hd ** -0.5 if scale is None else scale, int(causal), out.data_ptr(),
         None if lse is None else lse.data_ptr(),
         None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), _raw_stream(cache._index)), "nvfp4_kv_attention")
+        0 if workspace is None else workspace.numel(), _stream(cache)), "nvfp4_kv_attention")
     return (out, lse) if return_lse else out

@@ -144,3 +144,17 @@ def test_large_calls(dtype, hd, rows):
     (BF, 40003, 4, 16, 16), (F32, 2051, 1, 1024, 64)])      # the smallest and the largest rows
 def test_write_and_read_of_many_tokens(dtype, tokens, heads, hd, page_size):
     write_and_read(dtype, tokens, heads, hd, page_size, None, False)
+
+
+def test_refuses_a_cache_that_is_not_on_the_current_device():
+    """Kernels are launched on the current device: a cache of another one is refused, not read."""
+    case("kv cache on another device than the current one")
+    c = ref.make(4, BF, [1], [20], 2, 1, 64, 16)
+    cache = on_gpu(c)
+    cache._index += 1  # as if the current device had been changed
+    slots = torch.zeros(1, dtype=torch.int64, device=DEV)
+    k = torch.zeros(1, 1, 64, dtype=BF, device=DEV)
+    for call in (lambda: attend(c, cache), lambda: kvcache.read(cache, slots),
+                 lambda: kvcache.write(cache, k, k, slots)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
