@@ -36,10 +36,11 @@ __device__ __forceinline__ void load8(const void *x, int64_t e, float v[8]) {
 // Rows a lane takes at once, their loads issued together: without it a wave waits for one row's
 // slot and then its codes, and read ran at 3.5 TB/s (131072 tokens, 8 heads of 128: 200 us;
 // with 4 rows 143 us, 2 or 8 rows 3 to 8% slower). Write: 16384 tokens written and read 35.4 us
-// with 1 row, 34.2 with 2, 35.6 with 4. Calls of fewer values than kFewValues fill the chip with
-// one row a lane only (48 tokens written and read: 5.4 us, 7.3 us with 4).
+// with 1 row, 34.2 with 2, 35.6 with 4. Calls of fewer rows times lanes than these fill the chip
+// with one row a lane only (48 tokens written and read: 5.4 us, 7.3 us with 4; 4000 tokens of 5
+// heads of 64 read in fp32, 640 Ki: 5.2 us with 1, 4.5 with 4; 3000, 480 Ki: 4.4 either way).
 constexpr int kReadRows = 4, kWriteRows = 2;
-constexpr int64_t kFewValues = 4 << 20;
+constexpr int64_t kReadFew = 512 << 10, kWriteFew = 256 << 10;
 
 // Slots of this lane's U rows: a workgroup takes U x 256 / lanes; -1 past the end
 // and for tokens without a slot in the cache.
@@ -144,8 +145,9 @@ int launch_kv_write(const nvfp4_kv_cache &c, const void *k, const void *v, int d
   p.S[0] = c.S_k, p.S[1] = c.S_v;
   p.slots = slots, p.tokens = tokens, p.n_slots = c.pages * c.page_size;
   p.heads = (int)c.kv_heads, p.head_dim = (int)c.head_dim, p.page_shift = page_shift_of(c);
-  const int u = tokens * c.kv_heads * c.head_dim * 2 < kFewValues ? 1 : kWriteRows;
-  const dim3 g = row_grid(tokens, c.kv_heads, c.head_dim / 16, 2, u), b(256);
+  const int64_t lanes = c.head_dim / 16;
+  const int u = tokens * c.kv_heads * lanes * 2 < kWriteFew ? 1 : kWriteRows;
+  const dim3 g = row_grid(tokens, c.kv_heads, lanes, 2, u), b(256);
   if (dtype == NVFP4_DTYPE_BF16) {
     if (u == 1) hipLaunchKernelGGL((k_kv_write<NVFP4_DTYPE_BF16, 1>), g, b, 0, st, p);
     else hipLaunchKernelGGL((k_kv_write<NVFP4_DTYPE_BF16, kWriteRows>), g, b, 0, st, p);
@@ -227,8 +229,9 @@ int launch_kv_read(const nvfp4_kv_cache &c, const int64_t *slots, int64_t n, voi
   if (z == 0) return NVFP4_OK;
   p.slots = slots, p.n = n, p.n_slots = c.pages * c.page_size;
   p.heads = (int)c.kv_heads, p.head_dim = (int)c.head_dim, p.page_shift = page_shift_of(c);
-  const int u = n * c.kv_heads * c.head_dim * z < kFewValues ? 1 : kReadRows;
-  const dim3 g = row_grid(n, c.kv_heads, c.head_dim / read_values(out_dtype), z, u), b(256);
+  const int64_t lanes = c.head_dim / read_values(out_dtype);
+  const int u = n * c.kv_heads * lanes * z < kReadFew ? 1 : kReadRows;
+  const dim3 g = row_grid(n, c.kv_heads, lanes, z, u), b(256);
   if (out_dtype == NVFP4_DTYPE_F32) {
     if (u == 1) hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_F32, 1, true>), g, b, 0, st, p);
     else hipLaunchKernelGGL((k_kv_read<NVFP4_DTYPE_F32, kReadRows, true>), g, b, 0, st, p);
