@@ -68,6 +68,8 @@ struct Attn {
   float scale;
   int direct;    // one piece a row, written straight to out
   int first;     // workgroups of list[0]; the others are list[1]'s
+  int lead_len;  // tokens of the prefix, if the own tokens' workgroups take it first
+  const int32_t *lead;  // and its pages
   void *out;
   float *lse;
   List list[2];
@@ -485,15 +487,25 @@ struct RawRows {
   u4 q[NT][HD / 32][F32 ? 2 : 1];
 };
 
+// lim[n]: the first token of the job that the lane's row of tile n does not see.
+template <int NT>
+__device__ __forceinline__ void row_ends(const Attn &p, const Job &j, int r0, int rows, int i, int *lim) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int tok = min(r0 + 16 * n + i, rows - 1) / p.group;
+    lim[n] = j.causal ? min(j.len, j.len - j.nq + tok + 1) : j.len;
+  }
+}
+
 template <int HD, int NT, bool F32, bool EXACT>
 __device__ __forceinline__ void load_rows(const Attn &p, const Job &j, int h, int r0, int rows,
                                           int lane, RawRows<HD, NT, F32> &y, Rows<HD, NT, F32> &x) {
   const int i = lane & 15, quad = lane >> 4;
+  row_ends<NT>(p, j, r0, rows, i, x.lim);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int r = min(r0 + 16 * n + i, rows - 1);
     const int tok = r / p.group, head = h * p.group + (r - tok * p.group);
-    x.lim[n] = j.causal ? min(j.len, j.len - j.nq + tok + 1) : j.len;
     const int64_t at = (int64_t)(j.q0 + tok) * p.q_ts + head * p.q_hs + quad * (HD / 4);
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s)
@@ -852,7 +864,8 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
 // its products then goes ahead of one in its exponentials, which fills the gaps between
 // them (468 -> 444 us on two 2048-query chunks; at both products the same, at the second alone
 // 460). Eight waves: four (half the rows a dequantised group serves) take 515 us. The products
-// alone would take 257 us, the exponentials add about 100, dequantising 60, LDS reads 30.
+// alone would take 257 us, the exponentials add about 100, dequantising 60, LDS reads 30. With
+// `lead` the rows go over the prefix and then over their own tokens, and nothing is left to join.
 template <int HD, int NT, bool F32, bool EXACT, int W>
 __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   // Groups of a stage. At HD 256 LDS holds half as many: of eight waves two take a group, one its
@@ -868,22 +881,28 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   const int i = lane & 15, quad = lane >> 4;
   Share sh;
   if (!share_of(p, lane, sh)) return;
-  const Job j = sh.j;
-  const int h = sh.h, rows = j.nq * p.group, R0 = sh.rt * (16 * NT * W), t0 = sh.t0;
+  Job j = sh.j;
+  const int h = sh.h, rows = j.nq * p.group, R0 = sh.rt * (16 * NT * W);
   if (R0 >= rows) return;
   const float S_k = p.S_k[h], S_v = p.S_v[h];
-  int t1 = sh.t1;
   const int r0 = R0 + wave * 16 * NT;
 
-  int lim_lo, lim_hi, none;
-  row_limits(p, j, R0, min(R0 + 16 * NT * W, rows), none, lim_hi);
-  t1 = min(t1, lim_hi);
-  row_limits(p, j, min(r0, rows - 1), min(r0 + 16 * NT, rows), lim_lo, lim_hi);
-  if (r0 >= rows) lim_hi = 0;  // a wave without rows only dequantises
-
+  // the token list in hand, and what of it the wave's rows see
+  int t0 = sh.t0, t1 = sh.t1, lim_lo, lim_hi;
+  bool lead = p.lead_len > 0;
+  if (lead) j.pages = p.lead, j.len = p.lead_len, j.causal = 0, t0 = 0, t1 = p.lead_len;
+  Pages pg;
+  const auto open = [&]() {
+    int none;
+    row_limits(p, j, R0, min(R0 + 16 * NT * W, rows), none, lim_hi);
+    t1 = min(t1, lim_hi);
+    row_limits(p, j, min(r0, rows - 1), min(r0 + 16 * NT, rows), lim_lo, lim_hi);
+    if (r0 >= rows) lim_hi = 0;  // a wave without rows only dequantises
+    pg = open_pages(j, p.page_shift, t0, t1, lane);
+  };
+  open();
   Group<HD> g;
   int ok = 0;
-  Pages pg = open_pages(j, p.page_shift, t0, t1, lane);
   const int mine = wave % GS, part_kv = GS == W ? 3 : 1 + wave / GS;
   const auto fetch = [&](int t) {  // this wave's group of the stage at t
     t += 16 * mine;
@@ -917,74 +936,81 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
     __builtin_amdgcn_sched_barrier(0);
     use_rows<HD, NT, F32>(raw, p.scale * kLog2e * S_k, x);
   }
-  if (t0 < t1) {
-    dequantise(0);
-    if (t0 + STAGE < t1) fetch(t0 + STAGE);
-  }
-  __syncthreads();
-  int b = 0, t = t0;
-  for (; t < t1; advance(pg, j, p.page_shift, t1, lane))
-  for (const int te = min(t1, pg.t + kRun); t < te; t += STAGE, b ^= 1) {  // the stages of a run
-    // operands are read one step ahead of their products: the values' before the exponentials,
-    // the next tile's keys before the second product
-    // (at HD 256 they would not fit beside the sums)
-    constexpr bool AHEAD = HD <= 128;
-    const int tiles = min(GS / 2, (min(t1, lim_hi) - t + 31) >> 5);
-    h8 kf[AHEAD ? 2 * KS : 1];
-    if constexpr (AHEAD) {
-#pragma unroll
-      for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[b][k / KS][k % KS][lane];
-    }
-#pragma unroll 1
-    for (int c = 0; c < tiles; ++c) {
-      const int tt = t + 32 * c;
-      __builtin_amdgcn_s_setprio(1);
-      f4 s[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = (f4){0, 0, 0, 0};
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const h8 a = AHEAD ? kf[AHEAD ? u * KS + k : 0] : kfrag[b][2 * c + u][k][lane];
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int q = 0; q < HALVES; ++q)
-              s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, x.q[n][q][k], s[n][u], 0, 0, 0);
-        }
-      h8 vf[AHEAD ? DV : 1];
-      if constexpr (AHEAD) {
-#pragma unroll
-        for (int d = 0; d < DV; ++d) vf[d] = vfrag[b][c][d][lane];
-      }
-      const int seen = __builtin_amdgcn_readfirstlane(oks[b][2 * c] | oks[b][2 * c + 1] << 1);
-      __builtin_amdgcn_s_setprio(0);
-      __builtin_amdgcn_sched_barrier(0);
-      if (tt + 32 > lim_lo || seen != 3) hide<NT>(s, x.lim, tt, t1, seen, quad);
-      h8 pf[NT][HALVES];
-      probabilities<HD, NT, F32>(s, x, pf);
-      if constexpr (AHEAD) {
-        const int nc = min(c + 1, GS / 2 - 1);
-#pragma unroll
-        for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[b][2 * nc + k / KS][k % KS][lane];
-        __builtin_amdgcn_sched_barrier(0);
-      }
-#pragma unroll
-      for (int d = 0; d < DV; ++d) {
-        const h8 a = AHEAD ? vf[AHEAD ? d : 0] : vfrag[b][c][d][lane];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int q = 0; q < HALVES; ++q)
-            x.acc[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf[n][q], x.acc[n][d], 0, 0, 0);
-      }
-    }
-    if (t + STAGE < t1) {
-      dequantise(b ^ 1);
-      if (t + 2 * STAGE < t1) fetch(t + 2 * STAGE);
+  for (;;) {
+    if (t0 < t1) {
+      dequantise(0);
+      if (t0 + STAGE < t1) fetch(t0 + STAGE);
     }
     __syncthreads();
+    int b = 0;
+    for (int t = t0; t < t1; advance(pg, j, p.page_shift, t1, lane))
+    for (const int te = min(t1, pg.t + kRun); t < te; t += STAGE, b ^= 1) {  // the stages of a run
+      // operands are read one step ahead of their products: the values' before the exponentials,
+      // the next tile's keys before the second product
+      // (at HD 256 they would not fit beside the sums)
+      constexpr bool AHEAD = HD <= 128;
+      const int tiles = min(GS / 2, (min(t1, lim_hi) - t + 31) >> 5);
+      h8 kf[AHEAD ? 2 * KS : 1];
+      if constexpr (AHEAD) {
+  #pragma unroll
+        for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[b][k / KS][k % KS][lane];
+      }
+  #pragma unroll 1
+      for (int c = 0; c < tiles; ++c) {
+        const int tt = t + 32 * c;
+        __builtin_amdgcn_s_setprio(1);
+        f4 s[NT][2];
+  #pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = (f4){0, 0, 0, 0};
+  #pragma unroll
+        for (int k = 0; k < KS; ++k)
+  #pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const h8 a = AHEAD ? kf[AHEAD ? u * KS + k : 0] : kfrag[b][2 * c + u][k][lane];
+  #pragma unroll
+            for (int n = 0; n < NT; ++n)
+  #pragma unroll
+              for (int q = 0; q < HALVES; ++q)
+                s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, x.q[n][q][k], s[n][u], 0, 0, 0);
+          }
+        h8 vf[AHEAD ? DV : 1];
+        if constexpr (AHEAD) {
+  #pragma unroll
+          for (int d = 0; d < DV; ++d) vf[d] = vfrag[b][c][d][lane];
+        }
+        const int seen = __builtin_amdgcn_readfirstlane(oks[b][2 * c] | oks[b][2 * c + 1] << 1);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (tt + 32 > lim_lo || seen != 3) hide<NT>(s, x.lim, tt, t1, seen, quad);
+        h8 pf[NT][HALVES];
+        probabilities<HD, NT, F32>(s, x, pf);
+        if constexpr (AHEAD) {
+          const int nc = min(c + 1, GS / 2 - 1);
+  #pragma unroll
+          for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[b][2 * nc + k / KS][k % KS][lane];
+          __builtin_amdgcn_sched_barrier(0);
+        }
+  #pragma unroll
+        for (int d = 0; d < DV; ++d) {
+          const h8 a = AHEAD ? vf[AHEAD ? d : 0] : vfrag[b][c][d][lane];
+  #pragma unroll
+          for (int n = 0; n < NT; ++n)
+  #pragma unroll
+            for (int q = 0; q < HALVES; ++q)
+              x.acc[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf[n][q], x.acc[n][d], 0, 0, 0);
+        }
+      }
+      if (t + STAGE < t1) {
+        dequantise(b ^ 1);
+        if (t + 2 * STAGE < t1) fetch(t + 2 * STAGE);
+      }
+      __syncthreads();
+    }
+    if (!lead) break;
+    lead = false, j = sh.j, t0 = sh.t0, t1 = sh.t1;  // the own tokens
+    open();
+    row_ends<NT>(p, j, r0, rows, i, x.lim);
+    if (t0 < t1) fetch(t0);
   }
 
   // each lane holds HD/16 consecutive channels of its row four times
@@ -1123,6 +1149,7 @@ struct Plan {
   Part prefix, own;
   int direct;  // no partial sums
   int finish;  // the own tokens' workgroups add the prefix's pieces: no join
+  int lead;    // the own tokens' workgroups go over the prefix first: no pieces at all
 };
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1210,6 +1237,17 @@ Plan plan_of(const KvAttention &a) {
       const int64_t n = (int64_t)target + 1 + a.batch, most = a.batch * cdiv(a.max_kv, 128);
       r.slots = (int)(n < most ? n : most);
     }
+  }
+  // A short prefix that tiles of many rows read: the own tokens' workgroups go over it first. That
+  // saves the partial sums (2 KiB a row and head of 128, and the join; about as much time as the
+  // products of 1024 tokens) and costs the products of the rows that its tiles hold in vain (of ragged
+  // sequences half a tile each): 3 x 772 queries of 56 heads on 843 tokens, 79 before them: 84 -> 42
+  // us, 64 x up to 10 of 32 heads on 1000 behind 500: 46 -> 39. The other way round 32 x up to 65 on
+  // 2000 behind 1500: 167 us, 124 shared, and with few workgroups 16 x 64 on 64 behind 4000: 110, 81.
+  if (own && p.own.tile && p.own.target == 0.0f && p.prefix.slots && a.prefix_len <= a.max_kv) {
+    const int64_t tile = 16 * p.own.nt * p.own.waves, rows = a.tokens * G;
+    const int64_t vain = a.batch * (a.tokens == a.batch * a.max_q ? p.own.row_tiles * tile - a.max_q * G : tile / 2);
+    if ((double)a.prefix_len * (double)vain <= 1024.0 * (double)rows) p.lead = 1, p.prefix = Part{};
   }
   p.direct = p.prefix.slots == 0 ? p.own.target == 0.0f : p.prefix.slots == 1 && p.own.slots == 0;
   return p;
@@ -1303,6 +1341,7 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
   p.page_shift = __builtin_ctzll((unsigned long long)c.page_size);
   p.pages = (int)c.pages, p.max_q = (int)a.max_q, p.scale = a.scale, p.direct = plan.direct;
   p.out = a.out, p.lse = a.lse;
+  if (plan.lead) p.lead = a.prefix_pages, p.lead_len = (int)a.prefix_len;
   float *opart = static_cast<float *>(a.workspace), *own = opart + n_pre * c.head_dim;
   float2 *ml = reinterpret_cast<float2 *>(own + n_own * c.head_dim), *ml_own = ml + n_pre;
   int2 *where = reinterpret_cast<int2 *>(ml_own + n_own);

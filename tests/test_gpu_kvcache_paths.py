@@ -158,3 +158,20 @@ def test_refuses_a_cache_that_is_not_on_the_current_device():
                  lambda: kvcache.write(cache, k, k, slots)):
         with pytest.raises(ValueError, match="current device"):
             call()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("hd,prefix,causal", [(64, 700, True), (128, 77, True), (128, 129, False), (112, 1, True),
+                                              (256, 300, True), (144, 2100, True)])
+def test_prefix_before_own_tokens_in_one_workgroup(dtype, hd, prefix, causal):
+    """Sequences that fill tiles of their own go over the prefix first: large and small calls,
+    sequences without own tokens, without queries, with a hidden page in the prefix."""
+    case(f"kv attention, prefix {prefix} before own tokens, head_dim {hd}, {dtype}, causal {causal}")
+    q = [280, 279, 0, 3, 280, 1, 140, 31]
+    c = ref.make(prefix + hd, dtype, q, [1030, 750, 0, 517, 300, 1029, 800, 0], 16, 8, hd, 32, prefix)
+    check(c, attend(c, causal=causal), causal)
+    c = ref.make(prefix + hd + 1, dtype, [128, 5, 100], [128, 0, 110], 4, 2, hd, 16, prefix)
+    check(c, attend(c, causal=causal), causal)
+    if prefix > 200:
+        c["prefix_pages"][3] = -1
+        check(c, attend(c, causal=causal), causal)
