@@ -1166,14 +1166,18 @@ Part rows_part(const KvAttention &a, int64_t rows, int nt) {
 }
 
 // k_kv_attn_tile: workgroups a CU holds, by LDS (at HD 256 1 KiB a token, two stages).
-// Calls that tiles of 256 rows and pieces of 128 tokens would give fewer than 512 workgroups
-// take tiles of 64 rows (240 rows x 700 tokens of 8 heads 22.7 -> 17.0 us, 2000 x 2500 32 -> 29;
-// from 512 workgroups on equal or slower).
-Part tile_part(const KvAttention &a, int64_t rows, int64_t jobs, int64_t len) {
+// Tiles of 64 rows are taken where tiles of 256 rows and pieces of 128 tokens would give fewer than
+// 512 workgroups (240 rows x 700 tokens of 8 heads 22.7 -> 17.0 us, 2000 x 2500 32 -> 29), and for
+// up to 2048 own tokens where they fill the chip with whole contexts and the larger tiles would
+// have to be cut into pieces (8 heads, 2800 rows x 1000 tokens 52 -> 29 us, 1600 x 2000 54 -> 47,
+// 2 x 2000 x 2500 70 and 73). Elsewhere equal or slower.
+Part tile_part(const KvAttention &a, int64_t rows, int64_t jobs, int64_t len, bool own) {
   Part r = {};
-  const bool small = jobs * a.cache->kv_heads * cdiv(rows, 256) * cdiv(len, 128) < 512;
-  const int64_t hd = a.cache->head_dim;
+  const int64_t hd = a.cache->head_dim, n = jobs * a.cache->kv_heads;
   const bool wide = hd > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
+  const bool small = n * cdiv(rows, 256) * cdiv(len, 128) < 512 ||
+                     (own && len <= 2048 && n * cdiv(rows, wide || f32 ? 128 : 256) <= 170 &&
+                      n * cdiv(rows, 64) >= 192);
   r.tile = 1;
   r.nt = wide || f32 || small || rows <= 64 ? 1 : 2;
   r.waves = small || rows <= 64 * r.nt || (wide && f32) ? 4 : 8;
@@ -1184,8 +1188,8 @@ Part tile_part(const KvAttention &a, int64_t rows, int64_t jobs, int64_t len) {
 
 // Rows a (sequence, key/value head): up to 32 to k_kv_attn_rows, whose waves work alone; more to
 // k_kv_attn_tile, whose waves share what they dequantise.
-Part plan_rows(const KvAttention &a, int64_t rows, int64_t jobs, int64_t len) {
-  if (rows > 32) return tile_part(a, rows, jobs, len);
+Part plan_rows(const KvAttention &a, int64_t rows, int64_t jobs, int64_t len, bool own) {
+  if (rows > 32) return tile_part(a, rows, jobs, len, own);
   const bool one = rows <= 16 || (a.cache->head_dim > 128 && a.dtype == NVFP4_DTYPE_F32);
   return rows_part(a, rows, one ? 1 : 2);
 }
@@ -1194,9 +1198,9 @@ Plan plan_of(const KvAttention &a) {
   Plan p = {};
   const int64_t G = a.heads / a.cache->kv_heads, kvh = a.cache->kv_heads;
   const bool own = a.max_kv > 0 || a.prefix_len == 0;
-  if (own) p.own = plan_rows(a, a.max_q * G, a.batch, a.max_kv);
+  if (own) p.own = plan_rows(a, a.max_q * G, a.batch, a.max_kv, true);
   if (a.prefix_len > 0) {
-    p.prefix = plan_rows(a, a.tokens * G, 1, a.prefix_len);
+    p.prefix = plan_rows(a, a.tokens * G, 1, a.prefix_len, false);
     // one launch for both lists where the prefix is so short that the own tokens' kernel does it
     // in one round of 128-token pieces
     if (own && !p.own.tile) {
