@@ -12,7 +12,9 @@
  * A slot is page * page_size + offset. Which pages belong to which sequence is the caller's
  * (a block table); cache memory need not be initialised: bytes of tokens beyond a sequence's
  * length never reach a result, whatever they hold. Scale bytes are read as E4M3 magnitudes
- * with 0x7F coded as zero, as everywhere in the library.
+ * with 0x7F coded as zero, as everywhere in the library. A cache without pages may leave the codes
+ * and block scales NULL; S_k and S_v are needed by every call that has something to do, except that
+ * write has nothing to do then.
  *
  * Conventions (pointers, streams, status codes, rounding) are those of nvfp4.h, except that
  * k, v and q may be strided: the last dimension is contiguous, the strides of the token and the

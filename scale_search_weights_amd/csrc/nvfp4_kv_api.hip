@@ -19,11 +19,24 @@ bool mul_ok(int64_t a, int64_t b, int64_t *out) {
 
 hipStream_t as_stream(void *s) { return static_cast<hipStream_t>(s); }
 
+#define NVFP4_TRY(expr)               \
+  do {                                \
+    const int rc_ = (expr);           \
+    if (rc_ != NVFP4_OK) return rc_;  \
+  } while (0)
+
 int check_dtype(int dtype) {
   return dtype == NVFP4_DTYPE_F32 || dtype == NVFP4_DTYPE_BF16 ? NVFP4_OK : NVFP4_ERR_DTYPE;
 }
 
-// sizes of the cache, then its pointers (not needed when it has no pages or no heads)
+// the head scales: every kernel reads them, also those that only write zeros
+int check_scales(const nvfp4_kv_cache *c) {
+  if (!c->S_k || !c->S_v) return NVFP4_ERR_NULL;
+  return aligned(c->S_k, 4) && aligned(c->S_v, 4) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+}
+
+// sizes of the cache, then its pointers; without pages or heads it needs none here, and what
+// launches for it all the same checks the head scales
 int check_cache(const nvfp4_kv_cache *c, int64_t max_head_dim) {
   if (!c) return NVFP4_ERR_NULL;
   if (c->pages < 0 || c->pages > INT32_MAX || c->kv_heads < 0 || c->kv_heads > 65535)
@@ -34,12 +47,11 @@ int check_cache(const nvfp4_kv_cache *c, int64_t max_head_dim) {
   int64_t n;
   if (!mul_ok(c->pages * c->page_size, c->kv_heads * c->head_dim, &n)) return NVFP4_ERR_SHAPE;
   if (n == 0) return NVFP4_OK;
-  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales || !c->S_k || !c->S_v)
-    return NVFP4_ERR_NULL;
+  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return NVFP4_ERR_NULL;
   if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) ||
-      !aligned(c->v_scales, 16) || !aligned(c->S_k, 4) || !aligned(c->S_v, 4))
+      !aligned(c->v_scales, 16))
     return NVFP4_ERR_ALIGN;
-  return NVFP4_OK;
+  return check_scales(c);
 }
 
 // rows x[t][h] of a strided tensor: 16-byte pieces, offsets within int64
@@ -53,12 +65,6 @@ int check_rows(const void *x, int dtype, int64_t tokens, int64_t heads, int64_t 
   if ((ts * size) % 16 || (hs * size) % 16) return NVFP4_ERR_ALIGN;
   return NVFP4_OK;
 }
-
-#define NVFP4_TRY(expr)               \
-  do {                                \
-    const int rc_ = (expr);           \
-    if (rc_ != NVFP4_OK) return rc_;  \
-  } while (0)
 
 // Everything of an attention call but its pointers; fills what the plan needs.
 int check_attention(const nvfp4_kv_cache *c, int dtype, int64_t tokens, int64_t heads,
@@ -119,6 +125,7 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, const int64_t *slots, int64_t n, 
   NVFP4_TRY(check_cache(cache, 1024));
   if (n < 0 || n > INT32_MAX) return NVFP4_ERR_SHAPE;
   if (n == 0 || cache->kv_heads == 0) return NVFP4_OK;
+  NVFP4_TRY(check_scales(cache));
   if (!slots || (!k && !v)) return NVFP4_ERR_NULL;
   if (!aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16)) return NVFP4_ERR_ALIGN;
   const hipStream_t st = as_stream(stream);
@@ -152,6 +159,7 @@ int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const void *q, int dtype, in
   if (!q_offsets && batch * max_q != tokens) return NVFP4_ERR_SHAPE;
   if (!isfinite(scale)) return NVFP4_ERR_ARG;
   if (nothing(a)) return NVFP4_OK;
+  NVFP4_TRY(check_scales(cache));
   if (a.max_kv > table_width * cache->page_size) return NVFP4_ERR_SHAPE;
   if (!kv_attention_fits(a)) return NVFP4_ERR_SHAPE;
   if (!q || !out || (a.max_kv > 0 && (!kv_lens || !block_table)) ||
