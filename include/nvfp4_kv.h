@@ -80,7 +80,8 @@ NVFP4_API int nvfp4_kv_read(const nvfp4_kv_cache *cache, const int64_t *slots, i
  * (block_table and kv_lens are then not read and may be NULL).
  *   out[i][j] = sum_t p_t v_t,  p = softmax over the seen tokens of scale * (q[i][j] . k_t);
  *   lse[i][j] (nullable, fp32) = ln sum_t exp(scale * (q[i][j] . k_t)).
- * A row that sees nothing gets out = 0 and lse = -inf. Rows of out and lse that belong to no
+ * A row that sees nothing gets out = 0 and lse = -inf; any other row whose query is not finite gets
+ * NaN in both, and other rows stay right. Rows of out and lse that belong to no
  * sequence hold unspecified values. Page ids outside [0, pages) hide the page's tokens; kv_lens
  * is cut to [0, max_kv].
  *

@@ -232,6 +232,14 @@ __device__ __forceinline__ float row_factor(float amax, float &inverse) {
   return __uint_as_float((unsigned)(127 + e) << 23);
 }
 
+// The ends of a row with sum l over the maximum m (log2): the sums' factor and lse. A row that sees
+// nothing has l = 0 exactly, every other one at least 2^base (base_of), and a query that is not
+// finite NaN, which stays NaN: piece by piece, however many pieces there are.
+__device__ __forceinline__ float out_factor(float S_v, float l) { return l == 0.0f ? 0.0f : S_v / l; }
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.0f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(l));
+}
+
 // ---------------------------------------------------------------- raw groups of 16 tokens
 
 constexpr int more(int a) { return a > 1 ? a : 1; }
@@ -536,7 +544,7 @@ __device__ __forceinline__ void use_rows(const RawRows<HD, NT, F32> &y, float sc
     amax = fmaxf(amax, xor16(amax));
     amax = fmaxf(amax, xor32(amax));
     float inv;
-    const float f = row_factor(amax, inv) * sign;
+    const float f = row_factor(amax, inv) * (amax < INFINITY ? sign : NAN);  // infinite: all scores NaN
     x.c[n] = fmaxf(fabsf(scale) * inv, 1e-37f);  // positive, so a hidden score stays -inf
     x.off[n] = INFINITY;
     x.l[n] = 0.0f;
@@ -661,7 +669,7 @@ __device__ __forceinline__ void finish_rows(const Attn &p, const Job &j, int h, 
       const float2 ml = k0.ml[at + k * step];
       f4 o = {0, 0, 0, 0};
       if (in) o = *reinterpret_cast<const f4 *>(k0.opart + (at + k * step) * p.hd + 4 * c);
-      if (ml.y > 0.0f) {
+      if (ml.y != 0.0f) {
         const float to = fmaxf(M, ml.x);
         const float a = __builtin_amdgcn_exp2f(M - to), e = __builtin_amdgcn_exp2f(ml.x - to);
         M = to;
@@ -677,15 +685,15 @@ __device__ __forceinline__ void finish_rows(const Attn &p, const Job &j, int h, 
       L = 0.0f;
       y = (f4){0, 0, 0, 0};
       for (int k = 0; k < per; ++k) {
-        if (!(sml[2 * (g + k) + 1] > 0.0f)) continue;
+        if (sml[2 * (g + k) + 1] == 0.0f) continue;
         const float e = __builtin_amdgcn_exp2f(sml[2 * (g + k)] - M);
         L += sml[2 * (g + k) + 1] * e;
         y += so[(g + k) * LANES + c] * e;
       }
       const int r = r0 + i, tok = r / p.group, head = h * p.group + (r - tok * p.group);
       const int64_t to = (int64_t)(j.q0 + tok) * p.heads + head;
-      if (in) store4<F32>(p.out, to * p.hd + 4 * c, y * (L > 0.0f ? S_v / L : 0.0f));
-      if (c == 0 && p.lse) p.lse[to] = L > 0.0f ? kLn2 * (M + __builtin_amdgcn_logf(L)) : -INFINITY;
+      if (in) store4<F32>(p.out, to * p.hd + 4 * c, y * out_factor(S_v, L));
+      if (c == 0 && p.lse) p.lse[to] = row_lse(M, L);
     }
     __syncthreads();
   }
@@ -826,11 +834,11 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
 #pragma unroll
       for (int k = 0; k < W; ++k) {
         const float mk = sm_m[k][16 * n + row];
-        if (mk != -INFINITY) ll += sm_l[k][16 * n + row] * __builtin_amdgcn_exp2f(mk - mm);
+        if (sm_l[k][16 * n + row] != 0.0f) ll += sm_l[k][16 * n + row] * __builtin_amdgcn_exp2f(mk - mm);
       }
       const int tok = r / p.group, head = h * p.group + (r - tok * p.group);
       const int64_t at = (int64_t)(j.q0 + tok) * p.heads + head;
-      const float f = sh.direct ? (ll > 0.0f ? S_v / ll : 0.0f) : 1.0f;
+      const float f = sh.direct ? out_factor(S_v, ll) : 1.0f;
       for (int d = 2 * col; d < p.hd; d += 8 * W) {
         f2 y = {0.0f, 0.0f};
 #pragma unroll
@@ -841,7 +849,7 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
       }
       if (col == 0 && !finish) {
         if (sh.direct) {
-          if (p.lse) p.lse[at] = ll > 0.0f ? kLn2 * (mm - kBase + __builtin_amdgcn_logf(ll)) : -INFINITY;
+          if (p.lse) p.lse[at] = row_lse(mm - kBase, ll);
         } else {
           p.list[sh.list].ml[part + r] = make_float2(mm - kBase, ll);
         }
@@ -1024,7 +1032,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
     if (r >= rows) continue;
     const int tok = r / p.group, head = h * p.group + (r - tok * p.group);
     const int64_t at = (int64_t)(j.q0 + tok) * p.heads + head;
-    const float f = sh.direct ? (l > 0.0f ? S_v / l : 0.0f) : 1.0f;
+    const float f = sh.direct ? out_factor(S_v, l) : 1.0f;
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
       const int ch = DV * (4 * quad + r4);
@@ -1042,7 +1050,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
     }
     if (quad == 0) {
       if (sh.direct) {
-        if (p.lse) p.lse[at] = l > 0.0f ? kLn2 * (__builtin_amdgcn_logf(l) - x.off[n]) : -INFINITY;
+        if (p.lse) p.lse[at] = row_lse(-x.off[n], l);
       } else {
         p.list[sh.list].ml[part + r] = make_float2(-x.off[n], l);
       }
@@ -1106,7 +1114,7 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
     const float2 ml = (pre ? p.ml : p.ml_own)[row];
     f4 o = {0, 0, 0, 0};
     if (in) o = *reinterpret_cast<const f4 *>((pre ? p.opart : p.opart_own) + row * p.hd + 4 * c);
-    if (ml.y > 0.0f) {  // else the piece holds nothing the row sees
+    if (ml.y != 0.0f) {  // else the piece holds nothing the row sees
       const float to = fmaxf(M, ml.x);
       const float a = __builtin_amdgcn_exp2f(M - to), e = __builtin_amdgcn_exp2f(ml.x - to);
       M = to;
@@ -1122,15 +1130,14 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
   L = 0.0f;
   y = (f4){0, 0, 0, 0};
   for (int k = 0; k < p.per; ++k) {
-    if (!(sm_l[g + k] > 0.0f)) continue;
+    if (sm_l[g + k] == 0.0f) continue;
     const float e = __builtin_amdgcn_exp2f(sm_m[g + k] - M);
     L += sm_l[g + k] * e;
     y += so[g + k][c] * e;
   }
   const int64_t to = (int64_t)(lo + i) * p.heads + head;
-  const float f = L > 0.0f ? S_v / L : 0.0f;
-  if (in) store4<F32>(p.out, to * p.hd + 4 * c, y * f);
-  if (c == 0 && p.lse) p.lse[to] = L > 0.0f ? kLn2 * (M + __builtin_amdgcn_logf(L)) : -INFINITY;
+  if (in) store4<F32>(p.out, to * p.hd + 4 * c, y * out_factor(S_v, L));
+  if (c == 0 && p.lse) p.lse[to] = row_lse(M, L);
 }
 
 // ---------------------------------------------------------------- plan and launch
