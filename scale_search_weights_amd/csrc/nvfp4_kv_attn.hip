@@ -1229,14 +1229,19 @@ Plan plan_of(const KvAttention &a) {
     const float target = fmaxf(held - 0.5f * (float)a.batch, 0.75f * held);
     r.slots = (int)a.batch;
     // Short contexts: one piece a sequence, with more waves the fewer the sequences, saves the
-    // partial sums and the join (about 5 us); an iteration of such a workgroup costs about 2 us
+    // partial sums and the join (about 5 us); an iteration of such a workgroup costs 1 to 2 us
     // however little it reads, so the fewer workgroups there are to share the chip, the fewer
-    // iterations it may take. (32 heads of 128, 8 key/value heads: 30 x 6000 tokens 51.6 us cut
-    // into pieces, 44.7 us whole; 10 x 1000 13.4 and 12.1; 4 x 1000 10.7 and 11.5.)
+    // iterations it may take. Calls that are launched one by one need 12.7 us for two launches and
+    // 9 for one, calls from a graph only the GPU's time; a context is whole while that is faster in
+    // one way at little cost in the other. Cut and whole, us, one by one | from a graph, 8 key/value
+    // heads of 128: 4 x 1000 tokens 12.7, 11.6 | 10.6, 11.7; 4 x 1500 12.6, 14.1 | 12.2, 14.1; from a
+    // graph 10 x 1000 13.2, 12.0; 7 x 1200 13.4, 12.6; 7 x 1500 13.6, 13.9; 30 x 6000 43.0, 37.8. 20
+    // heads of 64: 1 x 1500 12.7, 11.3 | 10.4, 11.1; 5 x 1500 13.1, 11.3 | 13.1, 11.4.
     bool whole = a.max_kv <= 128;
     if (!r.tile && r.nt == 1 && a.cache->head_dim <= 128 && a.dtype != NVFP4_DTYPE_F32 &&
         !(p.prefix.slots && !p.prefix.tile)) {
-      const int64_t n = a.batch * units, most = n / 20 < 3 ? 3 : n / 20 > 12 ? 12 : n / 20;
+      const int64_t n = a.batch * units, least = a.cache->head_dim <= 64 || n > 40 ? 3 : 2;
+      const int64_t most = n / 20 < least ? least : n / 20 > 12 ? 12 : n / 20;
       const int w = n <= 256 ? 16 : n <= 512 ? 8 : 4;
       whole = a.max_kv <= 32 * w * most;
       if (whole) r.waves = w, p.finish = p.prefix.slots > 0;
