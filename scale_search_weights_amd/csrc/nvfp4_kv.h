@@ -4,6 +4,7 @@
 
 #include "../../include/nvfp4_kv.h"
 #include "nvfp4_internal.h"
+#include "nvfp4_kv_plan.h"
 
 namespace nvfp4 {
 
@@ -13,28 +14,6 @@ int launch_kv_write(const nvfp4_kv_cache &c, const void *k, const void *v, int d
 int launch_kv_read(const nvfp4_kv_cache &c, const int64_t *slots, int64_t n, void *k, void *v,
                    int out_dtype, hipStream_t st);
 
-struct KvAttention {
-  const nvfp4_kv_cache *cache;
-  const void *q;
-  int dtype;
-  int64_t tokens, heads, q_ts, q_hs, batch;
-  const int32_t *q_offsets;
-  int64_t max_q;
-  const int32_t *block_table;
-  int64_t table_width;
-  const int32_t *kv_lens;
-  int64_t max_kv;
-  const int32_t *prefix_pages;
-  int64_t prefix_len;
-  float scale;
-  int causal;
-  void *out;
-  float *lse;
-  void *workspace;
-};
-// whether every launch of the call fits a grid
-bool kv_attention_fits(const KvAttention &a);
-size_t kv_attention_workspace_size(const KvAttention &a);
 int launch_kv_attention(const KvAttention &a, hipStream_t st);
 
 // NVFP4_DEBUG_CHECKS: scan a strided [tokens][heads][head_dim] tensor for NaN and infinities.
