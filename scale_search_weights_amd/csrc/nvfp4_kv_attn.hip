@@ -68,6 +68,7 @@ struct Attn {
   float scale;
   int direct;    // one piece a row, written straight to out
   int first;     // workgroups of list[0]; the others are list[1]'s
+  int slot0;     // the launch's first slot of list[0]
   int lead_len;  // tokens of the prefix, if the own tokens' workgroups take it first
   const int32_t *lead;  // and its pages
   void *out;
@@ -183,12 +184,12 @@ __device__ __forceinline__ bool share_of(const Attn &p, int lane, Share &s) {
   // chip's eight dies in turn, fall on all of them
   int w = blockIdx.x;
   const int second = w >= p.first;
-  if (second) w -= p.first;
+  if (second) w -= p.first;  // only where both lists start at slot 0
   const List &k = p.list[second];
   s.h = w % p.kv_heads;
   w /= p.kv_heads;
   s.rt = k.row_tiles - 1 - w % k.row_tiles;  // the tiles that see most tokens first
-  const int slot = w / k.row_tiles;
+  const int slot = p.slot0 + w / k.row_tiles;
   s.direct = p.direct;
   if (k.prefix || k.target == 0.0f) {
     const int len = k.prefix || !p.kv_lens ? 0 : length_of(p.kv_lens, slot, p.batch, k.max_len);
@@ -1059,8 +1060,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
 }
 
 // Join the partial sums of the rows: HD / 4 lanes take four channels each; of a workgroup's
-// groups of such lanes `per` (a power of two, about the pieces of a row) share a row and take
-// its pieces in turn. The prefix's pieces come first, then those of the sequence's own tokens.
+// groups of such lanes `per` (join_per) share a row and take its pieces in turn. The prefix's pieces come first, then those of the sequence's own tokens.
 struct Join {
   const float *opart, *opart_own, *S_v;
   const float2 *ml, *ml_own;
@@ -1182,13 +1182,7 @@ void launch_hd(const Attn &p, const Part &r, unsigned grid, hipStream_t st) {
 }
 
 template <int HD>
-void launch_join(Join &p, const KvAttention &a, const Plan &plan, hipStream_t st) {
-  constexpr int GROUPS = 1024 / HD;
-  const float n = (float)plan.prefix.slots + plan.own.target / (float)a.batch;
-  p.per = 1;
-  while (p.per < GROUPS && (float)p.per < n) p.per *= 2;
-  const dim3 g((unsigned)cdiv(a.max_q * a.heads, GROUPS / p.per), (unsigned)a.batch);
-  const bool f32 = a.dtype == NVFP4_DTYPE_F32;
+void launch_join(const Join &p, bool f32, const dim3 &g, hipStream_t st) {
   if (f32) hipLaunchKernelGGL((k_kv_attn_join<HD, true>), g, dim3(256), 0, st, p);
   else hipLaunchKernelGGL((k_kv_attn_join<HD, false>), g, dim3(256), 0, st, p);
 }
@@ -1215,7 +1209,6 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
   const bool f32 = a.dtype == NVFP4_DTYPE_F32;
   List lists[2] = {};
   const Part parts[2] = {plan.prefix, plan.own};
-  const int64_t grids[2] = {part_grid(a, plan.prefix), part_grid(a, plan.own)};
   List &x = lists[0], &y = lists[1];
   x.table = a.prefix_pages, x.max_len = (int)a.prefix_len, x.prefix = 1;
   x.piece = plan.prefix.piece, x.opart = opart, x.ml = ml;
@@ -1224,29 +1217,25 @@ int launch_kv_attention(const KvAttention &a, hipStream_t st) {
   y.opart = own, y.ml = ml_own, y.where = where, y.finish = plan.finish;
   for (int k = 0; k < 2; ++k)
     lists[k].row_tiles = parts[k].row_tiles, lists[k].slots = parts[k].slots;
-  const auto launch = [&](int k, bool both) {
-    p.list[0] = lists[k], p.list[1] = lists[!k];
-    p.first = (int)grids[k];
-    const unsigned g = (unsigned)(grids[k] + (both ? grids[1] : 0));
-    if (f32) launch_hd<true>(p, parts[k], g, st);
-    else launch_hd<false>(p, parts[k], g, st);
-  };
-  const bool both = grids[0] && grids[1] && parts[0].nt == parts[1].nt &&
-                    parts[0].waves == parts[1].waves && parts[0].tile == parts[1].tile &&
-                    grids[0] + grids[1] <= INT32_MAX;
-  if (grids[0]) launch(0, both);
-  if (grids[1] && !both) launch(1, false);
-  if (!plan.direct && !plan.finish) {
-    Join x = {};
-    x.opart = opart, x.opart_own = own, x.ml = ml, x.ml_own = ml_own;
-    x.S_v = c.S_v, x.out = a.out, x.lse = a.lse, x.q_offsets = a.q_offsets, x.kv_lens = a.kv_lens;
-    x.tokens = p.tokens, x.heads = p.heads, x.kv_heads = p.kv_heads, x.group = p.group, x.hd = p.hd;
-    x.max_q = p.max_q, x.n_prefix = plan.prefix.slots;
-    x.where = plan.own.target > 0.0f ? where : nullptr;
-    if (p.hd <= 64) launch_join<64>(x, a, plan, st);
-    else if (p.hd <= 128) launch_join<128>(x, a, plan, st);
-    else launch_join<256>(x, a, plan, st);
-  }
+  Join jn = {};
+  jn.opart = opart, jn.opart_own = own, jn.ml = ml, jn.ml_own = ml_own;
+  jn.S_v = c.S_v, jn.out = a.out, jn.lse = a.lse, jn.q_offsets = a.q_offsets, jn.kv_lens = a.kv_lens;
+  jn.tokens = p.tokens, jn.heads = p.heads, jn.kv_heads = p.kv_heads, jn.group = p.group, jn.hd = p.hd;
+  jn.max_q = p.max_q, jn.n_prefix = plan.prefix.slots, jn.per = join_per(a, plan);
+  jn.where = plan.own.target > 0.0f ? where : nullptr;
+  each_launch(a, plan, [&](const Launch &l) {
+    if (l.list == 2) {
+      const dim3 g((unsigned)l.grid, (unsigned)a.batch);
+      if (p.hd <= 64) launch_join<64>(jn, f32, g, st);
+      else if (p.hd <= 128) launch_join<128>(jn, f32, g, st);
+      else launch_join<256>(jn, f32, g, st);
+      return;
+    }
+    p.list[0] = lists[l.list], p.list[1] = lists[!l.list];
+    p.first = (int)(l.both ? part_grid(a, plan.prefix) : l.grid), p.slot0 = l.slot0;
+    if (f32) launch_hd<true>(p, parts[l.list], (unsigned)l.grid, st);
+    else launch_hd<false>(p, parts[l.list], (unsigned)l.grid, st);
+  });
   return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 

@@ -3,6 +3,7 @@
 
 #include <limits.h>
 #include <math.h>
+#include <stdint.h>
 
 #include "../../include/nvfp4_kv.h"
 
@@ -166,10 +167,67 @@ inline int64_t own_rows(const KvAttention &a, const Plan &p) {
   return p.own.slots && !p.finish ? a.tokens * a.heads : 0;
 }
 
-// whether every launch of the call fits a grid
+// The join: groups of HD / 4 lanes in a workgroup of 256, and how many of them share a row (a power
+// of two, about the pieces of a row).
+inline int join_groups(const KvAttention &a) {
+  return a.cache->head_dim <= 64 ? 16 : a.cache->head_dim <= 128 ? 8 : 4;
+}
+inline int join_per(const KvAttention &a, const Plan &p) {
+  const float n = (float)p.prefix.slots + p.own.target / (float)a.batch;
+  int per = 1;
+  while (per < join_groups(a) && (float)per < n) per *= 2;
+  return per;
+}
+inline bool joins(const Plan &p) { return !p.direct && !p.finish; }
+inline int64_t join_grid(const KvAttention &a, const Plan &p) {
+  return cdiv(a.max_q * a.heads, join_groups(a) / join_per(a, p));
+}
+
+// HIP launches less than 2^32 threads a dimension. A part of more (many sequences behind a loose
+// max_q) goes in several launches of whole slots; 0 if one slot is too many.
+constexpr int64_t kMaxThreads = UINT32_MAX;
+inline int64_t slots_a_launch(const KvAttention &a, const Part &r) {
+  return kMaxThreads / (64 * r.waves) / (a.cache->kv_heads * r.row_tiles);
+}
+
+struct Launch {
+  int list;        // 0 the prefix, 1 own tokens, 2 the join
+  int both;        // the own tokens' workgroups follow the prefix's
+  int slot0;       // the first slot
+  int64_t grid;    // workgroups (of the prefix and the own tokens: all)
+  int threads;     // of a workgroup
+};
+
+// f(Launch) for every launch of the call, in order.
+template <typename F>
+void each_launch(const KvAttention &a, const Plan &p, F f) {
+  const int64_t n0 = part_grid(a, p.prefix), n1 = part_grid(a, p.own);
+  const bool both = n0 && n1 && p.prefix.nt == p.own.nt && p.prefix.waves == p.own.waves &&
+                    p.prefix.tile == p.own.tile && (n0 + n1) * 64 * p.own.waves <= kMaxThreads;
+  const auto part = [&](int k, const Part &r) {
+    const int64_t most = slots_a_launch(a, r);
+    for (int64_t at = 0; at < r.slots; at += most) {
+      const int64_t n = r.slots - at < most ? r.slots - at : most;
+      f(Launch{k, 0, (int)at, n * a.cache->kv_heads * r.row_tiles, 64 * r.waves});
+    }
+  };
+  if (both) {
+    f(Launch{0, 1, 0, n0 + n1, 64 * p.own.waves});
+  } else {
+    if (n0) part(0, p.prefix);
+    if (n1) part(1, p.own);
+  }
+  if (joins(p)) f(Launch{2, 0, 0, join_grid(a, p), 256});
+}
+
+// whether the call can be launched
 inline bool kv_attention_fits(const KvAttention &a) {
   const Plan p = plan_of(a);
-  return part_grid(a, p.prefix) <= INT32_MAX && part_grid(a, p.own) <= INT32_MAX;
+  for (int k = 0; k < 2; ++k) {
+    const Part &r = k ? p.own : p.prefix;
+    if (r.slots && (part_grid(a, r) > INT32_MAX || slots_a_launch(a, r) < 1)) return false;
+  }
+  return !joins(p) || join_grid(a, p) * 256 <= kMaxThreads;
 }
 
 inline size_t kv_attention_workspace_size(const KvAttention &a) {
