@@ -88,12 +88,8 @@ __device__ __forceinline__ Job job_of(const Attn &p, const List &k, int b, int l
   if (k.prefix) {
     j.q0 = 0, j.nq = p.tokens, j.len = k.max_len, j.causal = 0, j.pages = k.table;
   } else {
-    int lo = b * p.max_q, hi = lo + p.max_q;
-    if (p.q_offsets) {
-      lo = min(max(p.q_offsets[b], 0), p.tokens);
-      hi = min(max(p.q_offsets[b + 1], lo), min(p.tokens, lo + p.max_q));
-    }
-    j.q0 = lo, j.nq = hi - lo;
+    const Span s = rows_of(p.q_offsets, b, p.max_q, p.tokens);
+    j.q0 = s.lo, j.nq = s.hi - s.lo;
     j.len = len;
     j.causal = k.causal;
     j.pages = k.table + b * k.table_width;
@@ -1080,11 +1076,8 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
   const int g = threadIdx.x / LANES, c = threadIdx.x % LANES, first = g & -p.per;
   const int r = blockIdx.x * (GROUPS / p.per) + g / p.per;  // of the sequence: token, head
   const int i = r / p.heads, head = r - i * p.heads;
-  int lo = b * p.max_q, hi = lo + p.max_q;
-  if (p.q_offsets) {
-    lo = min(max(p.q_offsets[b], 0), p.tokens);
-    hi = min(max(p.q_offsets[b + 1], lo), min(p.tokens, lo + p.max_q));
-  }
+  const Span sp = rows_of(p.q_offsets, b, p.max_q, p.tokens);
+  const int lo = sp.lo, hi = sp.hi;
   int own0 = 0, n = p.n_prefix;
   if (p.where) {
     if (p.kv_lens[b] > 0) {

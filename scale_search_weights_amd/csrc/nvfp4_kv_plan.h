@@ -9,6 +9,25 @@
 
 namespace nvfp4 {
 
+#if defined(__HIPCC__)
+#define NVFP4_HD __host__ __device__
+#else
+#define NVFP4_HD
+#endif
+
+// Rows lo .. hi - 1 of the call are those of sequence b. Nothing here passes 32 bits: without offsets
+// batch * max_q is tokens, with them a loose max_q is cut to the rows that are left before it is added.
+struct Span {
+  int lo, hi;
+};
+inline NVFP4_HD Span rows_of(const int32_t *q_offsets, int b, int max_q, int tokens) {
+  if (!q_offsets) return {b * max_q, (b + 1) * max_q};
+  int lo = q_offsets[b], hi = q_offsets[b + 1];
+  lo = lo < 0 ? 0 : lo > tokens ? tokens : lo;
+  const int end = lo + (max_q < tokens - lo ? max_q : tokens - lo);
+  return {lo, hi < lo ? lo : hi > end ? end : hi};
+}
+
 struct KvAttention {
   const nvfp4_kv_cache *cache;
   const void *q;
