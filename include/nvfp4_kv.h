@@ -92,9 +92,9 @@ NVFP4_API int nvfp4_kv_read(const nvfp4_kv_cache *cache, const int64_t *slots, i
  * out: [tokens][heads][head_dim] contiguous, of `dtype`. Partial sums are joined in a fixed
  * order: results are bitwise reproducible for the same arguments and device.
  *
- * max_q may be loose, but the call then launches a workgroup for every 16 to 256 rows that it allows
- * each sequence and key/value head, with rows or without; more than 2^31 - 1 of them are refused
- * (NVFP4_ERR_SHAPE).
+ * tokens * heads is at most 2^31 - 1025. max_q may be loose, but the call then launches a workgroup
+ * for every 16 to 256 rows that it allows each sequence and key/value head, with rows or without;
+ * more than 2^31 - 1 of them are refused (NVFP4_ERR_SHAPE).
  *
  * workspace: 16-byte aligned, at least nvfp4_kv_attention_workspace_size() bytes (may be 0),
  * no initialisation needed; calls that share it must not overlap.

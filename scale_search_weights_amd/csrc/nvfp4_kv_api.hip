@@ -78,7 +78,8 @@ int check_attention(const nvfp4_kv_cache *c, int dtype, int64_t tokens, int64_t 
   if (batch > 65535 || max_q > tokens || max_kv > (1 << 30) || prefix_len > (1 << 30))
     return NVFP4_ERR_SHAPE;
   int64_t n;
-  if (!mul_ok(tokens, heads, &n) || n > INT32_MAX) return NVFP4_ERR_SHAPE;
+  // row indices are 32 bits up to the end of the last tile, at most 256 rows past the last row
+  if (!mul_ok(tokens, heads, &n) || n > INT32_MAX - 1024) return NVFP4_ERR_SHAPE;
   if (heads > 0 && (c->kv_heads == 0 || heads % c->kv_heads)) return NVFP4_ERR_SHAPE;
   *a = KvAttention{};
   a->cache = c, a->dtype = dtype, a->tokens = tokens, a->heads = heads, a->batch = batch;
