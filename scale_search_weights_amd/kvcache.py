@@ -96,15 +96,16 @@ class KVCache:
 
 
 _BF16, _F32, _I32, _INT64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream without a Stream object
-_current_device = torch._C._cuda_getDevice
 
 
 def _stream(cache: KVCache) -> int:
-    """The current stream; the cache's GPU has to be the current one, where kernels are launched."""
-    if _current_device() != cache._index:
-        raise ValueError(f"the cache is on {cache.device}, the current device is cuda:{_current_device()}")
-    return _raw_stream(cache._index)
+    """The current stream (without building a Stream object); the cache's GPU has to be
+    the current one, where kernels are launched. torch's functions are looked up here, not at import:
+    builds without GPU support lack them."""
+    device = torch._C._cuda_getDevice()
+    if device != cache._index:
+        raise ValueError(f"the cache is on {cache.device}, the current device is cuda:{device}")
+    return torch._C._cuda_getCurrentRawStream(cache._index)
 
 
 def _rows(t, name: str, cache: KVCache, heads: int | None):
