@@ -63,6 +63,12 @@ struct Plan {
   int lead;    // the own tokens' workgroups go over the prefix first: no pieces at all
 };
 
+constexpr int kCus = 256;  // compute units of the chip
+
+// Tiles of many rows cut the contexts into pieces only where the chip holds this many times the
+// workgroups that whole contexts make: a row's partial sums cost more than a workgroup's wait.
+constexpr float kTileCut = 1.5f;
+
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // k_kv_attn_rows with 16 NT rows a workgroup; workgroups a CU holds, by registers.
@@ -71,7 +77,7 @@ inline Part rows_part(const KvAttention &a, int64_t rows, int nt) {
   const bool wide = a.cache->head_dim > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
   const int one = wide ? 2 : (f32 ? 3 : 4);
   r.nt = nt, r.waves = 4;
-  r.resident = 256 * (nt == 1 ? one : (one + 1) / 2);
+  r.resident = kCus * (nt == 1 ? one : (one + 1) / 2);
   r.row_tiles = (int)cdiv(rows, 16 * nt);
   return r;
 }
@@ -79,20 +85,20 @@ inline Part rows_part(const KvAttention &a, int64_t rows, int nt) {
 // k_kv_attn_tile: workgroups a CU holds, by LDS (at HD 256 1 KiB a token, two stages).
 // Tiles of 64 rows are taken where tiles of 256 rows and pieces of 128 tokens would give fewer than
 // 512 workgroups (240 rows x 700 tokens of 8 heads 22.7 -> 17.0 us, 2000 x 2500 32 -> 29), and for
-// up to 2048 own tokens where they fill the chip with whole contexts and the larger tiles would
-// have to be cut into pieces (8 heads, 2800 rows x 1000 tokens 52 -> 29 us, 1600 x 2000 54 -> 47,
+// up to 2048 own tokens where they give three quarters of the CUs a whole context and the larger tiles
+// (one workgroup a CU) would have to be cut into pieces (8 heads, 2800 rows x 1000 tokens 52 -> 29 us, 1600 x 2000 54 -> 47,
 // 2 x 2000 x 2500 70 and 73). Elsewhere equal or slower.
 inline Part tile_part(const KvAttention &a, int64_t rows, int64_t jobs, int64_t len, bool own) {
   Part r = {};
   const int64_t hd = a.cache->head_dim, n = jobs * a.cache->kv_heads;
   const bool wide = hd > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
   const bool small = n * cdiv(rows, 256) * cdiv(len, 128) < 512 ||
-                     (own && len <= 2048 && n * cdiv(rows, wide || f32 ? 128 : 256) <= 170 &&
-                      n * cdiv(rows, 64) >= 192);
+                     (own && len <= 2048 && kTileCut * (float)(n * cdiv(rows, wide || f32 ? 128 : 256)) <= kCus &&
+                      4 * n * cdiv(rows, 64) >= 3 * kCus);
   r.tile = 1;
   r.nt = wide || f32 || small || rows <= 64 ? 1 : 2;
   r.waves = small || rows <= 64 * r.nt || (wide && f32) ? 4 : 8;
-  r.resident = 256 * (wide ? 1 : (hd > 64 || r.waves == 8 ? 8 / r.waves : 3));
+  r.resident = kCus * (wide ? 1 : (hd > 64 || r.waves == 8 ? 8 / r.waves : 3));
   r.row_tiles = (int)cdiv(rows, 16 * r.nt * r.waves);
   return r;
 }
@@ -150,9 +156,7 @@ inline Plan plan_of(const KvAttention &a) {
       whole = a.max_kv <= 32 * w * most;
       if (whole) r.waves = w, p.finish = p.prefix.slots > 0;
     }
-    // many rows: a row's partial sums cost more than a workgroup's wait, so only where there
-    // are far fewer workgroups than the chip holds
-    if (!whole && held >= (r.tile ? 1.5f * (float)a.batch : 1.0f)) {
+    if (!whole && held >= (r.tile ? kTileCut * (float)a.batch : 1.0f)) {
       r.target = target;
       const int64_t n = (int64_t)target + 1 + a.batch, most = a.batch * cdiv(a.max_kv, 128);
       r.slots = (int)(n < most ? n : most);
