@@ -9,11 +9,11 @@
 //
 // They are bound by memory: write moves 2 or 4 bytes in and 9/16 out per value, read the reverse.
 // 131072 tokens of 8 heads of 128 are read in 134 us, 5.1 TB/s, what a 1 GiB copy reaches; 16384
-// tokens are written and read in 34 us, 5.0 TB/s; 30000 in fp32 in 99 us, 5.7 TB/s (eight
+// tokens are written and read in 35 us, 5.0 TB/s; 30000 in fp32 in 100 us, 5.6 TB/s (eight
 // values a lane of read, two strided stores, cost 74 us more). Values that are read back are stored
-// non-temporally (134 us, 143 with ordinary stores), except in rows of no whole 64 bytes (19103
-// tokens of 11 heads of 112: 20 us, 28 non-temporally); codes are not, the attention that follows
-// finds them in the caches.
+// non-temporally (134 us, 141 with ordinary stores), except in rows of no whole 64 bytes (19103
+// tokens of 11 heads of 112: 21 us, 29 non-temporally; 101071 of 12 heads of 80: 130 and 158); codes
+// are not, the attention that follows finds them in the caches.
 #include "nvfp4_device.h"
 #include "nvfp4_kv.h"
 
@@ -34,11 +34,11 @@ __device__ __forceinline__ void load8(const void *x, int64_t e, float v[8]) {
 }
 
 // Rows a lane takes at once, their loads issued together: without it a wave waits for one row's
-// slot and then its codes, and read ran at 3.5 TB/s (131072 tokens, 8 heads of 128: 200 us;
-// with 4 rows 143 us, 2 or 8 rows 3 to 8% slower). Write: 16384 tokens written and read 35.4 us
+// slot and then its codes, and read runs at 3.5 TB/s (131072 tokens, 8 heads of 128: 198 us;
+// with 4 rows 134 us, 2 or 8 rows 3 to 8% slower). Write: 16384 tokens written and read 35.4 us
 // with 1 row, 34.2 with 2, 35.6 with 4. Calls of fewer rows times lanes than these fill the chip
-// with one row a lane only (48 tokens written and read: 5.4 us, 7.3 us with 4; 4000 tokens of 5
-// heads of 64 read in fp32, 640 Ki: 5.2 us with 1, 4.5 with 4; 3000, 480 Ki: 4.4 either way).
+// with one row a lane only (48 tokens written and read: 5.5 us, 6.5 us with several; 4000 tokens of
+// 5 heads of 64 read in fp32, 640 Ki: 5.4 us with 1, 5.3 with 4; 3000, 480 Ki: 4.7 and 4.5).
 constexpr int kReadRows = 4, kWriteRows = 2;
 constexpr int64_t kReadFew = 512 << 10, kWriteFew = 256 << 10;
 
@@ -56,7 +56,7 @@ __device__ __forceinline__ void load_slots(const int64_t *slots, int64_t n, int6
 // The (head, first token, token step) of a workgroup. Large calls (DIES): workgroups go to the 8
 // dies in turn, and those of one chunk of tokens follow each other on one die, so that lines shared
 // by neighbouring heads meet in its L2. (With heads far apart in the grid: rows of 160 bytes, 101071
-// tokens of 12 heads, 213 us read, 131 so; rows of 512, 30000 tokens written and read, 116 and 99.
+// tokens of 12 heads, 213 us read, 130 so; rows of 512, 30000 tokens written and read, 116 and 100.
 // In small calls that order costs 0.3 to 1 us.)
 struct Place {
   int h;

@@ -15,10 +15,10 @@
 // [i HD/16, ..) of the value tokens 4 quad + 0..3 and 16 + 4 quad + 0..3.
 //
 // Two kernels. With up to 32 rows a (sequence, key/value head) the cache is read at the rate of
-// memory: k_kv_attn_rows, every wave dequantising its own tokens in registers (about 250 vector
+// memory: k_kv_attn_rows, every wave dequantising its own tokens in registers (about 260 vector
 // instructions for 32 tokens and 16 rows; 524000 tokens of 8 heads of 128, 604 MB, in 117 us,
 // 5.2 TB/s). With more rows the products bound it: k_kv_attn_tile, where the waves share what they
-// dequantise through LDS (2 x 2048 queries of 32 heads on 8192 tokens, 481 GFLOP, in 430 us,
+// dequantise through LDS (2 x 2048 queries of 32 heads on 8192 tokens, 481 GFLOP, in 433 us,
 // 1.1 PFLOP/s). The sequence axis is cut into pieces where there are few rows; their sums are
 // joined in a fixed order, by k_kv_attn_join or, where only a prefix is cut, by the workgroups of
 // the sequences' own tokens (finish_rows).
@@ -863,18 +863,18 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
 
 // Many query rows over one token list (a shared prefix, a prompt): each of W waves holds 16 NT
 // rows. A stage is 16 W tokens: every wave dequantises a group of 16 into LDS, as ready MFMA
-// operands in lane order (no bank conflicts), and all waves read all tiles. Two stages
+// operands in lane order (bank conflicts in 3% of the cycles), and all waves read all tiles. Two stages
 // are in LDS, so the next one is dequantised beside the products of this one by whichever
 // wave comes to it. Score products run at a raised wave priority: of a SIMD's two waves, one in
 // its products then goes ahead of one in its exponentials, which fills the gaps between
-// them (468 -> 444 us on two 2048-query chunks; at both products the same, at the second alone
-// 460). Eight waves: four (half the rows a dequantised group serves) take 515 us. The products
-// alone would take 257 us, the exponentials add about 100, dequantising 60, LDS reads 30. With
-// `lead` the rows go over the prefix and then over their own tokens, and nothing is left to join.
+// them (456 -> 433 us on two 2048-query chunks; at both products the same, at the second alone
+// in between). Eight waves: four (half the rows a dequantised group serves) take 495 us. Matrix
+// instructions hold the SIMDs for 43% of the time and vector instructions (exponentials,
+// dequantising) issue for 46% of it, so what is left to overlap is small. With `lead` the rows go over the prefix and then over their own tokens, and nothing is left to join.
 template <int HD, int NT, bool F32, bool EXACT, int W>
 __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   // Groups of a stage. At HD 256 LDS holds half as many: of eight waves two take a group, one its
-  // keys, one its values, against four waves on a SIMD each: 2000 x 4000 queries 244 -> 164 us. In
+  // keys, one its values, against four waves on a SIMD each: 2000 x 4000 queries 229 -> 169 us. In
   // fp32 eight cost 172 us against 152 (2 x 1000 x 3000): four.
   constexpr int GS = HD > 128 && W > 4 ? W / 2 : W, STAGE = 16 * GS;
   constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, KS = HD / 32;

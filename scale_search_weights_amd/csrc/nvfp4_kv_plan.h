@@ -84,10 +84,11 @@ inline Part rows_part(const KvAttention &a, int64_t rows, int nt) {
 
 // k_kv_attn_tile: workgroups a CU holds, by LDS (at HD 256 1 KiB a token, two stages).
 // Tiles of 64 rows are taken where tiles of 256 rows and pieces of 128 tokens would give fewer than
-// 512 workgroups (240 rows x 700 tokens of 8 heads 22.7 -> 17.0 us, 2000 x 2500 32 -> 29), and for
-// up to 2048 own tokens where they give three quarters of the CUs a whole context and the larger tiles
-// (one workgroup a CU) would have to be cut into pieces (8 heads, 2800 rows x 1000 tokens 52 -> 29 us, 1600 x 2000 54 -> 47,
-// 2 x 2000 x 2500 70 and 73). Elsewhere equal or slower.
+// 512 workgroups (8 heads, 240 rows x 700 tokens 23 -> 17 us, 500 x 2500 34 -> 30), and for up to 2048
+// own tokens where they give three quarters of the CUs a whole context and the larger tiles (one
+// workgroup a CU) would have to be cut into pieces (2800 rows x 1000 tokens 51 -> 28 us, 1600 x 2000
+// 54 -> 47). On longer contexts it goes either way (larger, smaller: 2000 rows x 2500 tokens 59, 52;
+// 2 x 2000 x 2500 69, 72); elsewhere equal or slower.
 inline Part tile_part(const KvAttention &a, int64_t rows, int64_t jobs, int64_t len, bool own) {
   Part r = {};
   const int64_t hd = a.cache->head_dim, n = jobs * a.cache->kv_heads;
@@ -134,7 +135,7 @@ inline Plan plan_of(const KvAttention &a) {
     Part &r = p.own;
     const int64_t units = kvh * r.row_tiles;
     // pieces wanted: with the half piece that a sequence adds on average, as many as the chip
-    // holds at once (64 sequences of 512 to 8192 tokens: 55 -> 49 us against not counting it)
+    // holds at once (64 sequences of 512 to 8192 tokens: 52 -> 48 us against not counting it)
     const float held = (float)r.resident / (float)units;
     const float target = fmaxf(held - 0.5f * (float)a.batch, 0.75f * held);
     r.slots = (int)a.batch;
@@ -165,9 +166,9 @@ inline Plan plan_of(const KvAttention &a) {
   // A short prefix that tiles of many rows read: the own tokens' workgroups go over it first. That
   // saves the partial sums (2 KiB a row and head of 128, and the join; about as much time as the
   // products of 1024 tokens) and costs the products of the rows that its tiles hold in vain (of ragged
-  // sequences half a tile each): 3 x 772 queries of 56 heads on 843 tokens, 79 before them: 84 -> 42
-  // us, 64 x up to 10 of 32 heads on 1000 behind 500: 46 -> 39. The other way round 32 x up to 65 on
-  // 2000 behind 1500: 167 us, 124 shared, and with few workgroups 16 x 64 on 64 behind 4000: 110, 81.
+  // sequences half a tile each): 3 x up to 772 queries of 56 heads on 843 tokens, 79 before them: 83
+  // -> 41 us, 64 x up to 10 of 32 heads on 1000 behind 500: 47 -> 39. The other way round 32 x up to
+  // 65 on 2000 behind 1500: 170 us, 127 shared, and 16 x 64 on 64 behind 4000: 112, 105.
   if (own && p.own.tile && p.own.target == 0.0f && p.prefix.slots && a.prefix_len <= a.max_kv) {
     const int64_t tile = 16 * p.own.nt * p.own.waves, rows = a.tokens * G;
     const int64_t vain = a.batch * (a.tokens == a.batch * a.max_q ? p.own.row_tiles * tile - a.max_q * G : tile / 2);

@@ -4,8 +4,8 @@ A ``KVCache`` holds one layer's pages: packed E2M1 codes and E4M3 block scales o
 values, and one fp32 tensor scale per head. ``write`` quantises new keys and values into
 cache slots, ``read`` dequantises slots, ``attention`` attends over the cached tokens of each
 sequence and of a prefix shared by the whole batch. As in ``nvfp4``, this module checks and
-marshals arguments; the work is done by the HIP kernels on the current stream, and there is
-no CPU fallback.
+marshals arguments; the work is done by the HIP kernels on the current stream, there is
+no CPU fallback, and no gradient flows through the results.
 
     cache = kvcache.KVCache.empty(pages, page_size, kv_heads, head_dim, S_k, S_v)
     kvcache.write(cache, k, v, slots)                       # slot = page * page_size + offset
