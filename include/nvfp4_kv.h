@@ -14,7 +14,7 @@
  * length never reach a result, whatever they hold. Scale bytes are read as E4M3 magnitudes
  * with 0x7F coded as zero, as everywhere in the library. A cache without pages may leave the codes
  * and block scales NULL; S_k and S_v are needed by every call that has something to do, except that
- * write has nothing to do then.
+ * write has nothing to do then, and append only queries to turn.
  *
  * Conventions (pointers, streams, status codes, rounding) are those of nvfp4.h, except that
  * k, v and q may be strided: the last dimension is contiguous, the strides of the token and the
@@ -26,6 +26,7 @@
 #define NVFP4_KV_H
 
 #include "nvfp4.h"
+#include "nvfp4_rotary.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -51,6 +52,26 @@ NVFP4_API int nvfp4_kv_write(const nvfp4_kv_cache *cache, const void *k, const v
                              int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
                              int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
                              void *stream);
+
+/*
+ * Append: nvfp4_kv_write with the rotation of nvfp4_rotate on the way. For every token t with
+ * 0 <= slots[t] < pages * page_size, k[t][h] turned by the token's positions and v[t][h] as it is go
+ * to slot slots[t] of head h; a turned key is quantised from its fp32 value, without a rounding to
+ * bf16 in between. Tokens with any other slot are skipped. Two tokens of one call must not share a
+ * slot. q_out[t][j] = q[t][j] turned, for every token, skipped ones too: q, q_out
+ * [tokens][heads][head_dim] of `dtype`, strided; q_out may be q itself, with the same strides, and
+ * must not overlap anything else that the call reads. heads 0 for none (q, q_out may then be NULL).
+ * k, v: [tokens][kv_heads][head_dim] of `dtype`, strided; slots: [tokens] int64; positions as in
+ * nvfp4_rotate. The rotation's pairs are a multiple of 8. All of it in one launch.
+ */
+NVFP4_API int nvfp4_kv_append(const nvfp4_kv_cache *cache, const nvfp4_rotary *rotary,
+                              const int64_t *positions, int64_t position_stride, const void *q,
+                              const void *k, const void *v, int dtype, int64_t tokens,
+                              int64_t heads, int64_t q_token_stride, int64_t q_head_stride,
+                              int64_t k_token_stride, int64_t k_head_stride,
+                              int64_t v_token_stride, int64_t v_head_stride, void *q_out,
+                              int64_t q_out_token_stride, int64_t q_out_head_stride,
+                              const int64_t *slots, void *stream);
 
 /*
  * Read cached keys and values back: k[n][h], v[n][h] = the values of slot slots[n], dequantised
@@ -111,6 +132,29 @@ NVFP4_API int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const void *q, int
                                  const int32_t *prefix_pages, int64_t prefix_len, float scale,
                                  int causal, void *out, float *lse, void *workspace,
                                  size_t workspace_bytes, void *stream);
+
+/*
+ * Attention over a sliding window and the first tokens, which stay visible (sinks): as
+ * nvfp4_kv_attention without a prefix, except that row i of a sequence's n, at position P = kv_lens[b] -
+ * n + i, sees the tokens t <= P with t > P - window or t < sinks. window is 1 to 2^30, sinks 0 to 2^30.
+ * Only tokens that some row of a tile of at most 256 rows sees are read (in groups of 16): the work and
+ * the workspace do not grow with the context, and the pages of tokens between the sinks' and the
+ * windows' groups may be gone from the block table (any ids there). Results are reproducible as
+ * there; a window that covers the context sees what nvfp4_kv_attention sees.
+ */
+NVFP4_API size_t nvfp4_kv_window_attention_workspace_size(const nvfp4_kv_cache *cache, int dtype,
+                                                          int64_t tokens, int64_t heads,
+                                                          int64_t batch, int64_t max_q,
+                                                          int64_t max_kv, int64_t window,
+                                                          int64_t sinks);
+NVFP4_API int nvfp4_kv_window_attention(const nvfp4_kv_cache *cache, const void *q, int dtype,
+                                        int64_t tokens, int64_t heads, int64_t q_token_stride,
+                                        int64_t q_head_stride, int64_t batch,
+                                        const int32_t *q_offsets, int64_t max_q,
+                                        const int32_t *block_table, int64_t table_width,
+                                        const int32_t *kv_lens, int64_t max_kv, int64_t window,
+                                        int64_t sinks, float scale, void *out, float *lse,
+                                        void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -18,7 +18,8 @@ PROBE_OUT = os.path.join(PKG, "libnvfp4_probe.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["nvfp4_api.hip", "nvfp4_quant.hip", "nvfp4_search.hip", "nvfp4_hessian.hip",
            "nvfp4_calib.hip", "nvfp4_ste.hip", "nvfp4_gram.hip", "nvfp4_gptq.hip", "nvfp4_debug.hip",
-           "nvfp4_noalloc.hip", "nvfp4_kv.hip", "nvfp4_kv_attn.hip", "nvfp4_kv_api.hip"]
+           "nvfp4_noalloc.hip", "nvfp4_kv.hip", "nvfp4_kv_attn.hip", "nvfp4_kv_api.hip",
+           "nvfp4_kv_window.hip", "nvfp4_kv_window_api.hip", "nvfp4_rotary.hip", "nvfp4_rotary_api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

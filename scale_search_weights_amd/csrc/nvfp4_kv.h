@@ -15,6 +15,7 @@ int launch_kv_read(const nvfp4_kv_cache &c, const int64_t *slots, int64_t n, voi
                    int out_dtype, hipStream_t st);
 
 int launch_kv_attention(const KvAttention &a, hipStream_t st);
+int launch_kv_window_attention(const KvAttention &a, int64_t window, int64_t sinks, hipStream_t st);
 
 // NVFP4_DEBUG_CHECKS: scan a strided [tokens][heads][head_dim] tensor for NaN and infinities.
 void debug_check_finite_rows(const void *x, int dtype, int64_t tokens, int64_t heads,

@@ -16,22 +16,9 @@
 // are not, the attention that follows finds them in the caches.
 #include "nvfp4_device.h"
 #include "nvfp4_kv.h"
+#include "nvfp4_rows.h"
 
 namespace nvfp4 {
-
-template <int DT>
-__device__ __forceinline__ void load8(const void *x, int64_t e, float v[8]) {
-  if (DT == NVFP4_DTYPE_BF16) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + e);
-    v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
-    v[4] = bf16_lo(w.z), v[5] = bf16_hi(w.z), v[6] = bf16_lo(w.w), v[7] = bf16_hi(w.w);
-  } else {
-    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + e);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
-}
 
 // Rows a lane takes at once, their loads issued together: without it a wave waits for one row's
 // slot and then its codes, and read runs at 3.5 TB/s (131072 tokens, 8 heads of 128: 198 us;
@@ -103,18 +90,8 @@ __global__ void __launch_bounds__(256) k_kv_write(KvWrite p) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (slot[u] < 0) continue;
-      float amax = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[u][i]));
-      const int b = max_scale_byte_fast(amax, lo6, hi6, S);
-      uint2 c = {0u, 0u};
-      if (b) {
-        const double sS = e4m3_value_d(b) * (double)S;
-        float lo, hi;
-        recip_bracket(sS, lo, hi);
-        c.x = fp4_clear_neg_zero(fp4_exact_codes8(v[u], lo, hi, sS));
-        c.y = fp4_clear_neg_zero(fp4_exact_codes8(v[u] + 8, lo, hi, sS));
-      }
+      uint2 c;
+      const int b = quantise16(v[u], lo6, hi6, S, c);
       const int64_t at = (((slot[u] >> p.page_shift) * p.heads + h) << p.page_shift) + (slot[u] & mask);
       reinterpret_cast<uint2 *>(p.codes[kv])[at * lanes + part] = c;
       p.scales[kv][at * lanes + part] = (uint8_t)b;

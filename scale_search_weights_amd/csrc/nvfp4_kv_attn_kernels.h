@@ -76,6 +76,8 @@ struct Attn {
   void *out;
   float *lse;
   List list[2];
+  int window, sinks;  // a window's call: tokens that a row sees up to its own, and first tokens always seen
+  int pieces;         // and the pieces of every row tile's tokens
 };
 
 // One sequence's share of the call.
@@ -168,6 +170,30 @@ struct Share {
   int h, rt, t0, t1, direct, list, slot;
 };
 
+// Where a row tile's tokens lie. Without a window they are counted as they are. With one they are the
+// first `cut` (the sinks, up to a whole group of 16), then what its rows' windows cover, `shift`
+// further on, from the group of the first row's first token: pieces, tiles and page ids count without
+// the gap, and only loads and masks go back to the token.
+template <bool WIN>
+struct Where {
+  int cut, shift;
+  __device__ __forceinline__ int token(int t) const { return WIN && t >= cut ? t + shift : t; }
+  __device__ __forceinline__ int index(int t) const { return WIN ? t - shift : t; }  // of a token behind the gap
+};
+
+// The row tile that begins with row r0. Positions before the sequence's first token (more rows than
+// tokens) have no window and no gap.
+template <bool WIN>
+__device__ __forceinline__ Where<WIN> where_of(const Attn &p, const Job &j, int r0) {
+  Where<WIN> w = {0, 0};
+  if constexpr (WIN) {
+    const int first = max(j.len - j.nq + r0 / p.group, 0) - p.window + 1;  // of the first row's window
+    w.cut = p.sinks + 15 & ~15;
+    w.shift = max((first & ~15) - w.cut, 0);
+  }
+  return w;
+}
+
 // The job's first partial row. A slot holds the rows of all tokens (prefix), of one sequence (own
 // tokens in pieces), or, of own tokens in one piece, the rows of all tokens are one slot.
 __device__ __forceinline__ int64_t part_of(const Attn &p, const Share &s) {
@@ -177,6 +203,7 @@ __device__ __forceinline__ int64_t part_of(const Attn &p, const Share &s) {
   return ((int64_t)s.h * p.tokens + s.j.q0) * p.group;
 }
 
+template <bool WIN>
 __device__ __forceinline__ bool share_of(const Attn &p, int lane, Share &s) {
   // slots last: those without a piece come at the end, and the pieces, which are dealt to the
   // chip's eight dies in turn, fall on all of them
@@ -189,6 +216,15 @@ __device__ __forceinline__ bool share_of(const Attn &p, int lane, Share &s) {
   s.rt = k.row_tiles - 1 - w % k.row_tiles;  // the tiles that see most tokens first
   const int slot = p.slot0 + w / k.row_tiles;
   s.direct = p.direct;
+  if constexpr (WIN) {  // slots: the pieces of every sequence; which tokens, the row tile says (piece_of)
+    const int b = slot / p.pieces;
+    s.j = job_of(p, k, b, p.kv_lens ? length_of(p.kv_lens, b, p.batch, k.max_len) : 0);
+    s.t0 = slot - b * p.pieces;
+    if (!p.direct && s.t0 == 0 && s.h == 0 && s.rt == 0 && threadIdx.x == 0)
+      k.where[b] = make_int2(slot, p.pieces);  // for the join
+    s.list = 0, s.slot = slot;
+    return true;
+  }
   if (k.prefix || k.target == 0.0f) {
     const int len = k.prefix || !p.kv_lens ? 0 : length_of(p.kv_lens, slot, p.batch, k.max_len);
     s.j = job_of(p, k, k.prefix ? 0 : slot, len);
@@ -271,19 +307,22 @@ struct Pages {
   int t, ids, next;
 };
 
-__device__ __forceinline__ int load_ids(const Job &j, int page_shift, int t, int t_end, int lane) {
+template <bool WIN>
+__device__ __forceinline__ int load_ids(const Job &j, Where<WIN> w, int page_shift, int t, int t_end, int lane) {
   t += 16 * lane;
-  return t < t_end ? j.pages[t >> page_shift] : -1;
+  return t < t_end ? j.pages[w.token(t) >> page_shift] : -1;
 }
 
-__device__ __forceinline__ Pages open_pages(const Job &j, int page_shift, int t0, int t_end, int lane) {
-  return {t0, load_ids(j, page_shift, t0, t_end, lane), load_ids(j, page_shift, t0 + kRun, t_end, lane)};
+template <bool WIN>
+__device__ __forceinline__ Pages open_pages(const Job &j, Where<WIN> w, int page_shift, int t0, int t_end, int lane) {
+  return {t0, load_ids(j, w, page_shift, t0, t_end, lane), load_ids(j, w, page_shift, t0 + kRun, t_end, lane)};
 }
 
-__device__ __forceinline__ void advance(Pages &pg, const Job &j, int page_shift, int t_end, int lane) {
+template <bool WIN>
+__device__ __forceinline__ void advance(Pages &pg, const Job &j, Where<WIN> w, int page_shift, int t_end, int lane) {
   pg.t += kRun;
   pg.ids = pg.next;
-  pg.next = load_ids(j, page_shift, pg.t + kRun, t_end, lane);
+  pg.next = load_ids(j, w, page_shift, pg.t + kRun, t_end, lane);
 }
 
 __device__ __forceinline__ int page_of(const Pages &pg, int t) {
@@ -571,17 +610,40 @@ __device__ __forceinline__ void row_limits(const Attn &p, const Job &j, int r0, 
   }
 }
 
+// The tokens t0 .. t1 - 1 (without the gap) of the share's piece, of rows that see none from hi on.
+__device__ __forceinline__ void piece_of(const Attn &p, Where<true> w, int hi, int &t0, int &t1) {
+  const int n = w.index(hi), per = ((n + 127 >> 7) + p.pieces - 1) / p.pieces << 7;
+  t0 *= per;
+  t1 = min(n, t0 + per);
+}
+
+// Whether some row does not see all of the tile's 32 tokens, when every row sees the tokens from `near`
+// up to lo and the sinks.
+template <bool WIN>
+__device__ __forceinline__ bool masked(const Attn &p, Where<WIN> gap, int t, int lo, int near) {
+  if constexpr (!WIN) return t + 32 > lo;
+  const int end = gap.token(t + 16) + 16;
+  return end > lo || (gap.token(t) < near && end > p.sinks);
+}
+
 // Scores of hidden tokens of the tile at t: -inf.
-template <int NT>
-__device__ __forceinline__ void hide(f4 (*s)[2], const int *lim, int t, int t1, int ok, int quad) {
+template <int NT, bool WIN>
+__device__ __forceinline__ void hide(f4 (*s)[2], const Attn &p, Where<WIN> gap, const int *lim, int t, int t1,
+                                     int ok, int quad) {
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int tt = t + 16 * u + 4 * quad + r;
-        if (tt >= lim[n] || tt >= t1 || !((ok >> u) & 1)) s[n][u][r] = -INFINITY;
+        if constexpr (WIN) {  // a piece ends with a tile, or where no row sees anything
+          const int tt = gap.token(t + 16 * u) + 4 * quad + r;
+          if (tt >= lim[n] || (tt < max(lim[n], 0) - p.window && tt >= p.sinks) || !((ok >> u) & 1))
+            s[n][u][r] = -INFINITY;
+        } else {
+          const int tt = t + 16 * u + 4 * quad + r;
+          if (tt >= lim[n] || tt >= t1 || !((ok >> u) & 1)) s[n][u][r] = -INFINITY;
+        }
       }
 }
 
@@ -700,7 +762,7 @@ __device__ __forceinline__ void finish_rows(const Attn &p, const Job &j, int h, 
 
 // W waves take the 32-token tiles of a piece in turn, each for the same 16 NT query rows, and
 // join their sums at the end.
-template <int HD, int NT, bool F32, bool EXACT, int W>
+template <int HD, int NT, bool F32, bool EXACT, int W, bool WIN>
 __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) k_kv_attn_rows(Attn p) {
   constexpr int HALVES = F32 ? 2 : 1, DV = HD / 16, OROW = HD + 4;
   constexpr float kBase = base_of(F32);
@@ -711,20 +773,23 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int i = lane & 15, quad = lane >> 4;
   Share sh;
-  if (!share_of(p, lane, sh)) return;
+  if (!share_of<WIN>(p, lane, sh)) return;
   const Job j = sh.j;
-  const int h = sh.h, rows = j.nq * p.group, r0 = sh.rt * (16 * NT), t0 = sh.t0;
+  const int h = sh.h, rows = j.nq * p.group, r0 = sh.rt * (16 * NT);
   if (r0 >= rows) return;
   const float S_k = p.S_k[h], S_v = p.S_v[h];
-  int t1 = sh.t1;
+  int t0 = sh.t0, t1 = sh.t1;
 
   int lim_lo, lim_hi;
   row_limits(p, j, r0, min(r0 + 16 * NT, rows), lim_lo, lim_hi);
-  t1 = min(t1, lim_hi);
+  const Where<WIN> gap = where_of<WIN>(p, j, r0);
+  if constexpr (WIN) piece_of(p, gap, lim_hi, t0, t1);
+  else t1 = min(t1, lim_hi);
+  const int near = WIN ? lim_hi - p.window : 0;  // the last row's window begins here
 
   Group<HD> g[2], nxt[2];  // raw codes: this tile's, and the next one's on their way
   int ok = 0, nxt_ok = 0;
-  Pages pg = open_pages(j, p.page_shift, t0, t1, lane);
+  Pages pg = open_pages(j, gap, p.page_shift, t0, t1, lane);
   Rows<HD, NT, F32> x;
   int t = t0 + 32 * wave;
   {
@@ -734,19 +799,19 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
     if (t < t1) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        ok |= load_group<HD, EXACT>(p, page_of(pg, t + 16 * u), h, t + 16 * u, lane, g[u]) << u;
+        ok |= load_group<HD, EXACT>(p, page_of(pg, t + 16 * u), h, gap.token(t + 16 * u), lane, g[u]) << u;
     }
     __builtin_amdgcn_sched_barrier(0);
     use_rows<HD, NT, F32>(raw, p.scale * kLog2e * S_k, x);
   }
-  for (; t < t1; advance(pg, j, p.page_shift, t1, lane))
+  for (; t < t1; advance(pg, j, gap, p.page_shift, t1, lane))
   for (const int te = min(t1, pg.t + kRun); t < te; t += 32 * W) {  // the tiles of a run
     if (t + 32 * W < t1) {
       nxt_ok = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int tt = t + 32 * W + 16 * u;
-        nxt_ok |= load_group<HD, EXACT>(p, page_of(pg, tt), h, tt, lane, nxt[u]) << u;
+        nxt_ok |= load_group<HD, EXACT>(p, page_of(pg, tt), h, gap.token(tt), lane, nxt[u]) << u;
       }
     }
     f4 s[NT][2];
@@ -767,7 +832,7 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
       __builtin_amdgcn_sched_barrier(0);  // one group's operands at a time: registers
     }
     order_wave_lds();
-    if (t + 32 > lim_lo || ok != 3) hide<NT>(s, x.lim, t, t1, ok, quad);
+    if (masked(p, gap, t, lim_lo, near) || ok != 3) hide<NT>(s, p, gap, x.lim, t, t1, ok, quad);
     h8 pf[NT][HALVES];
     probabilities<HD, NT, F32>(s, x, pf);
     __builtin_amdgcn_sched_barrier(0);
@@ -873,7 +938,7 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
 // in between). Eight waves: four (half the rows a dequantised group serves) take 495 us. Matrix
 // instructions hold the SIMDs for 43% of the time and vector instructions (exponentials,
 // dequantising) issue for 46% of it, so what is left to overlap is small. With `lead` the rows go over the prefix and then over their own tokens, and nothing is left to join.
-template <int HD, int NT, bool F32, bool EXACT, int W>
+template <int HD, int NT, bool F32, bool EXACT, int W, bool WIN>
 __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   // Groups of a stage. At HD 256 LDS holds half as many: of eight waves two take a group, one its
   // keys, one its values, against four waves on a SIMD each: 2000 x 4000 queries 229 -> 169 us. In
@@ -887,7 +952,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int i = lane & 15, quad = lane >> 4;
   Share sh;
-  if (!share_of(p, lane, sh)) return;
+  if (!share_of<WIN>(p, lane, sh)) return;
   Job j = sh.j;
   const int h = sh.h, rows = j.nq * p.group, R0 = sh.rt * (16 * NT * W);
   if (R0 >= rows) return;
@@ -898,14 +963,19 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   int t0 = sh.t0, t1 = sh.t1, lim_lo, lim_hi;
   bool lead = p.lead_len > 0;
   if (lead) j.pages = p.lead, j.len = p.lead_len, j.causal = 0, t0 = 0, t1 = p.lead_len;
+  const Where<WIN> gap = where_of<WIN>(p, j, R0);
+  int near = 0;  // the wave's last row's window begins here
   Pages pg;
   const auto open = [&]() {
     int none;
     row_limits(p, j, R0, min(R0 + 16 * NT * W, rows), none, lim_hi);
-    t1 = min(t1, lim_hi);
+    if constexpr (WIN) piece_of(p, gap, lim_hi, t0, t1);
+    else t1 = min(t1, lim_hi);
     row_limits(p, j, min(r0, rows - 1), min(r0 + 16 * NT, rows), lim_lo, lim_hi);
+    if constexpr (WIN) near = lim_hi - p.window;
+    lim_hi = gap.index(lim_hi);
     if (r0 >= rows) lim_hi = 0;  // a wave without rows only dequantises
-    pg = open_pages(j, p.page_shift, t0, t1, lane);
+    pg = open_pages(j, gap, p.page_shift, t0, t1, lane);
   };
   open();
   Group<HD> g;
@@ -913,7 +983,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   const int mine = wave % GS, part_kv = GS == W ? 3 : 1 + wave / GS;
   const auto fetch = [&](int t) {  // this wave's group of the stage at t
     t += 16 * mine;
-    ok = load_group<HD, EXACT>(p, page_of(pg, t), h, t, lane, g, part_kv);
+    ok = load_group<HD, EXACT>(p, page_of(pg, t), h, gap.token(t), lane, g, part_kv);
   };
   const auto dequantise = [&](int b) {
     if (part_kv & 2) stage_value_scales<HD, EXACT>(g, lane, vs_lds[mine]);
@@ -950,7 +1020,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
     }
     __syncthreads();
     int b = 0;
-    for (int t = t0; t < t1; advance(pg, j, p.page_shift, t1, lane))
+    for (int t = t0; t < t1; advance(pg, j, gap, p.page_shift, t1, lane))
     for (const int te = min(t1, pg.t + kRun); t < te; t += STAGE, b ^= 1) {  // the stages of a run
       // operands are read one step ahead of their products: the values' before the exponentials,
       // the next tile's keys before the second product
@@ -988,7 +1058,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
         const int seen = __builtin_amdgcn_readfirstlane(oks[b][2 * c] | oks[b][2 * c + 1] << 1);
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
-        if (tt + 32 > lim_lo || seen != 3) hide<NT>(s, x.lim, tt, t1, seen, quad);
+        if (masked(p, gap, tt, lim_lo, near) || seen != 3) hide<NT>(s, p, gap, x.lim, tt, t1, seen, quad);
         h8 pf[NT][HALVES];
         probabilities<HD, NT, F32>(s, x, pf);
         if constexpr (AHEAD) {
@@ -1057,6 +1127,60 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   }
 }
 
+// ---------------------------------------------------------------- launch
+
+template <int HD, bool F32, bool EXACT, bool WIN>
+void launch_rows(const Attn &p, const Part &r, unsigned grid, hipStream_t st) {
+  const dim3 g(grid), b(64 * r.waves);
+  if (r.tile) {
+    if (r.waves == 8) {
+      if constexpr (HD <= 128 || !F32)
+        hipLaunchKernelGGL((k_kv_attn_tile<HD, F32 || (HD > 128) ? 1 : 2, F32, EXACT, 8, WIN>), g, b, 0, st, p);
+    } else if (r.nt == 1) {
+      hipLaunchKernelGGL((k_kv_attn_tile<HD, 1, F32, EXACT, 4, WIN>), g, b, 0, st, p);
+    } else if constexpr (HD <= 128 && !F32) {
+      hipLaunchKernelGGL((k_kv_attn_tile<HD, 2, F32, EXACT, 4, WIN>), g, b, 0, st, p);
+    }
+  } else if (r.waves > 4) {
+    if constexpr (HD <= 128 && !F32) {
+      if (r.waves == 16) hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT, 16, WIN>), g, b, 0, st, p);
+      else hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT, 8, WIN>), g, b, 0, st, p);
+    }
+  } else if (r.nt == 1) {
+    hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT, 4, WIN>), g, b, 0, st, p);
+  } else if constexpr (HD <= 128 || !F32) {
+    hipLaunchKernelGGL((k_kv_attn_rows<HD, 2, F32, EXACT, 4, WIN>), g, b, 0, st, p);
+  }
+}
+
+template <int HD, bool F32, bool WIN>
+void launch_exact(const Attn &p, const Part &r, unsigned grid, hipStream_t st) {
+  if (p.hd == HD) launch_rows<HD, F32, true, WIN>(p, r, grid, st);
+  else launch_rows<HD, F32, false, WIN>(p, r, grid, st);
+}
+
+template <bool F32, bool WIN>
+void launch_hd(const Attn &p, const Part &r, unsigned grid, hipStream_t st) {
+  if (p.hd <= 64) launch_exact<64, F32, WIN>(p, r, grid, st);
+  else if (p.hd <= 128) launch_exact<128, F32, WIN>(p, r, grid, st);
+  else launch_exact<256, F32, WIN>(p, r, grid, st);
+}
+
+// What kernels need of a call, but the lists and the plan.
+inline Attn attn_of(const KvAttention &a) {
+  const nvfp4_kv_cache &c = *a.cache;
+  Attn p = {};
+  p.kc = c.k_codes, p.ks = c.k_scales, p.vc = c.v_codes, p.vs = c.v_scales;
+  p.S_k = c.S_k, p.S_v = c.S_v;
+  p.q = a.q, p.q_ts = a.q_ts, p.q_hs = a.q_hs, p.q_offsets = a.q_offsets, p.kv_lens = a.kv_lens;
+  p.tokens = (int)a.tokens, p.heads = (int)a.heads, p.kv_heads = (int)c.kv_heads;
+  p.group = (int)(a.heads / c.kv_heads), p.hd = (int)c.head_dim, p.batch = (int)a.batch;
+  p.page_shift = __builtin_ctzll((unsigned long long)c.page_size);
+  p.pages = (int)c.pages, p.max_q = (int)a.max_q, p.scale = a.scale;
+  p.out = a.out, p.lse = a.lse;
+  return p;
+}
+
 // Join the partial sums of the rows: HD / 4 lanes take four channels each; of a workgroup's
 // groups of such lanes `per` (join_per) share a row and take its pieces in turn. The prefix's pieces come first, then those of the sequence's own tokens.
 struct Join {
@@ -1069,70 +1193,14 @@ struct Join {
   int tokens, heads, kv_heads, group, hd, max_q, n_prefix, per;
 };
 
-template <int HD, bool F32>
-__global__ void __launch_bounds__(256) k_kv_attn_join(Join p) {
-  constexpr int LANES = HD / 4, GROUPS = 256 / LANES;
-  __shared__ f4 so[GROUPS][LANES];
-  __shared__ float sm_m[GROUPS], sm_l[GROUPS];
-  const int b = blockIdx.y;
-  const int g = threadIdx.x / LANES, c = threadIdx.x % LANES, first = g & -p.per;
-  const int r = blockIdx.x * (GROUPS / p.per) + g / p.per;  // of the sequence: token, head
-  const int i = r / p.heads, head = r - i * p.heads;
-  const Span sp = rows_of(p.q_offsets, b, p.max_q, p.tokens);
-  const int lo = sp.lo, hi = sp.hi;
-  int own0 = 0, n = p.n_prefix;
-  if (p.where) {
-    if (p.kv_lens[b] > 0) {
-      const int2 x = p.where[b];
-      if (x.y == 1 && n == 0) return;  // written by its only piece
-      own0 = x.x, n += x.y;
-    }
-  } else if (p.kv_lens) {
-    n += 1;
-  }
-  const bool here = lo + i < hi;
-  const int h = head / p.group, gr = head - h * p.group;
-  const float S_v = p.S_v[h];
-  const int64_t rows = (int64_t)p.tokens * p.group, own_rows = (int64_t)p.max_q * p.group;
-  const int64_t at = h * rows + (int64_t)(lo + i) * p.group + gr;  // in a slot of all tokens
-  const int64_t own_at =
-      p.where ? ((int64_t)own0 * p.kv_heads + h) * own_rows + (int64_t)i * p.group + gr : at;
-  const int64_t step = rows * p.kv_heads, own_step = own_rows * p.kv_heads;
-  float M = -INFINITY, L = 0.0f;
-  f4 y = {0, 0, 0, 0};
-  const bool in = 4 * c < p.hd;
-  if (!here) n = 0;
-#pragma unroll 4
-  for (int k = g - first; k < n; k += p.per) {
-    const bool pre = k < p.n_prefix;
-    const int64_t row = pre ? at + k * step : own_at + (k - p.n_prefix) * own_step;
-    const float2 ml = (pre ? p.ml : p.ml_own)[row];
-    f4 o = {0, 0, 0, 0};
-    if (in) o = *reinterpret_cast<const f4 *>((pre ? p.opart : p.opart_own) + row * p.hd + 4 * c);
-    if (ml.y != 0.0f) {  // else the piece holds nothing the row sees
-      const float to = fmaxf(M, ml.x);
-      const float a = __builtin_amdgcn_exp2f(M - to), e = __builtin_amdgcn_exp2f(ml.x - to);
-      M = to;
-      L = L * a + ml.y * e;
-      y = y * a + o * e;
-    }
-  }
-  if (c == 0) sm_m[g] = M, sm_l[g] = L;
-  so[g][c] = y;
-  __syncthreads();
-  if (g != first || !here) return;
-  for (int k = 1; k < p.per; ++k) M = fmaxf(M, sm_m[g + k]);
-  L = 0.0f;
-  y = (f4){0, 0, 0, 0};
-  for (int k = 0; k < p.per; ++k) {
-    if (sm_l[g + k] == 0.0f) continue;
-    const float e = __builtin_amdgcn_exp2f(sm_m[g + k] - M);
-    L += sm_l[g + k] * e;
-    y += so[g + k][c] * e;
-  }
-  const int64_t to = (int64_t)(lo + i) * p.heads + head;
-  if (in) store4<F32>(p.out, to * p.hd + 4 * c, y * out_factor(S_v, L));
-  if (c == 0 && p.lse) p.lse[to] = row_lse(M, L);
+// The join of a call whose own tokens lie in pieces behind n_prefix pieces of a prefix.
+inline Join join_of(const Attn &p, int n_prefix, int per) {
+  Join j = {};
+  j.S_v = p.S_v, j.out = p.out, j.lse = p.lse, j.q_offsets = p.q_offsets, j.kv_lens = p.kv_lens;
+  j.tokens = p.tokens, j.heads = p.heads, j.kv_heads = p.kv_heads, j.group = p.group, j.hd = p.hd;
+  j.max_q = p.max_q, j.n_prefix = n_prefix, j.per = per;
+  return j;
 }
+void launch_kv_join(const Join &p, bool f32, const dim3 &g, hipStream_t st);
 
 }  // namespace nvfp4

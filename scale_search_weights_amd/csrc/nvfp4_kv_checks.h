@@ -2,6 +2,7 @@
 #pragma once
 
 #include <limits.h>
+#include <math.h>
 
 #include "nvfp4_kv.h"
 
@@ -62,6 +63,72 @@ inline int check_rows(const void *x, int dtype, int64_t tokens, int64_t heads, i
     return NVFP4_ERR_SHAPE;
   if ((ts * size) % 16 || (hs * size) % 16) return NVFP4_ERR_ALIGN;
   return NVFP4_OK;
+}
+
+// Everything of an attention call but its pointers; fills what the plan needs.
+inline int check_attention(const nvfp4_kv_cache *c, int dtype, int64_t tokens, int64_t heads,
+                    int64_t batch, int64_t max_q, int64_t max_kv, int64_t prefix_len,
+                    KvAttention *a) {
+  NVFP4_TRY(check_dtype(dtype));
+  NVFP4_TRY(check_cache(c, 256));
+  if (tokens < 0 || heads < 0 || batch < 0 || max_q < 0 || max_kv < 0 || prefix_len < 0)
+    return NVFP4_ERR_SHAPE;
+  if (tokens > INT32_MAX || heads > INT32_MAX) return NVFP4_ERR_SHAPE;
+  if (batch > 65535 || max_q > tokens || max_kv > (1 << 30) || prefix_len > (1 << 30))
+    return NVFP4_ERR_SHAPE;
+  int64_t n;
+  // row indices are 32 bits up to the end of the last tile, at most 256 rows past the last row
+  if (!mul_ok(tokens, heads, &n) || n > INT32_MAX - 1024) return NVFP4_ERR_SHAPE;
+  if (heads > 0 && (c->kv_heads == 0 || heads % c->kv_heads)) return NVFP4_ERR_SHAPE;
+  *a = KvAttention{};
+  a->cache = c, a->dtype = dtype, a->tokens = tokens, a->heads = heads, a->batch = batch;
+  a->max_q = max_q, a->max_kv = c->pages ? max_kv : 0, a->prefix_len = c->pages ? prefix_len : 0;
+  return NVFP4_OK;
+}
+
+inline bool nothing(const KvAttention &a) {
+  return a.tokens == 0 || a.heads == 0 || a.batch == 0 || a.max_q == 0;
+}
+
+// The call's pointers and strides, into `a` of check_attention; fits() says whether the call's launches
+// are possible. A call with nothing to do passes.
+template <typename Fits>
+inline int check_attention_call(KvAttention *a, const void *q, int64_t q_ts, int64_t q_hs, const int32_t *q_offsets,
+                                const int32_t *block_table, int64_t table_width, const int32_t *kv_lens,
+                                const int32_t *prefix_pages, float scale, void *out, float *lse, Fits fits) {
+  const nvfp4_kv_cache *cache = a->cache;
+  if (table_width < 0 || table_width > INT32_MAX) return NVFP4_ERR_SHAPE;
+  if (!q_offsets && a->batch * a->max_q != a->tokens) return NVFP4_ERR_SHAPE;
+  if (!isfinite(scale)) return NVFP4_ERR_ARG;
+  if (nothing(*a)) return NVFP4_OK;
+  NVFP4_TRY(check_scales(cache));
+  if (a->max_kv > table_width * cache->page_size) return NVFP4_ERR_SHAPE;
+  if (!fits()) return NVFP4_ERR_SHAPE;
+  if (!q || !out || (a->max_kv > 0 && (!kv_lens || !block_table)) || (a->prefix_len > 0 && !prefix_pages))
+    return NVFP4_ERR_NULL;
+  if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(q_offsets, 4) || !aligned(block_table, 4) ||
+      !aligned(kv_lens, 4) || !aligned(prefix_pages, 4))
+    return NVFP4_ERR_ALIGN;
+  NVFP4_TRY(check_rows(q, a->dtype, a->tokens, a->heads, q_ts, q_hs));
+  a->q = q, a->q_ts = q_ts, a->q_hs = q_hs, a->q_offsets = q_offsets;
+  a->block_table = block_table, a->table_width = table_width;
+  a->kv_lens = a->max_kv > 0 ? kv_lens : nullptr;
+  a->prefix_pages = prefix_pages, a->scale = scale, a->out = out, a->lse = lse;
+  return NVFP4_OK;
+}
+
+inline int check_workspace(size_t need, const void *workspace, size_t bytes) {
+  if (need && (!workspace || bytes < need)) return NVFP4_ERR_WORKSPACE;
+  return need && !aligned(workspace, 16) ? NVFP4_ERR_ALIGN : NVFP4_OK;
+}
+
+inline void debug_check_attention(const KvAttention &a, hipStream_t st) {
+  if (!debug_checks_enabled()) return;
+  debug_check_finite_rows(a.q, a.dtype, a.tokens, a.heads, a.cache->head_dim, a.q_ts, a.q_hs, st);
+  if (a.cache->pages > 0) {
+    debug_check_scale(a.cache->S_k, a.cache->kv_heads, st);
+    debug_check_scale(a.cache->S_v, a.cache->kv_heads, st);
+  }
 }
 
 }  // namespace nvfp4

@@ -2,8 +2,9 @@
 
 A ``KVCache`` holds one layer's pages: packed E2M1 codes and E4M3 block scales of keys and
 values, and one fp32 tensor scale per head. ``write`` quantises new keys and values into
-cache slots, ``read`` dequantises slots, ``attention`` attends over the cached tokens of each
-sequence and of a prefix shared by the whole batch. As in ``nvfp4``, this module checks and
+cache slots, ``append`` does so with the keys turned by their positions on the way, ``read``
+dequantises slots, ``attention`` attends over the cached tokens of each sequence and of a prefix
+shared by the whole batch. As in ``nvfp4``, this module checks and
 marshals arguments; the work is done by the HIP kernels on the current stream, there is
 no CPU fallback, and no gradient flows through the results.
 
@@ -19,9 +20,11 @@ import torch
 
 from . import nvfp4
 from .nvfp4 import _I, _I64, _P, _SZ, _arg, _check, _dt, _need
+from .rotary import Rotary, _positions, _row_strides
 
 MAX_HEAD_DIM = 1024            # write, read
 MAX_ATTENTION_HEAD_DIM = 256
+MAX_WINDOW = 1 << 30           # also sinks
 
 
 class _Cache(ctypes.Structure):
@@ -32,10 +35,15 @@ class _Cache(ctypes.Structure):
 
 _SIGS = {
     "nvfp4_kv_write": (_I, [_P, _P, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P]),
+    "nvfp4_kv_append": (_I, [_P, _P, _P, _I64, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64,
+                             _P, _I64, _I64, _P, _P]),
     "nvfp4_kv_read": (_I, [_P, _P, _I64, _P, _P, _I, _P]),
     "nvfp4_kv_attention_workspace_size": (_SZ, [_P, _I, _I64, _I64, _I64, _I64, _I64, _I64]),
     "nvfp4_kv_attention": (_I, [_P, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P,
                                 _I64, _P, _I64, ctypes.c_float, _I, _P, _P, _P, _SZ, _P]),
+    "nvfp4_kv_window_attention_workspace_size": (_SZ, [_P, _I, _I64, _I64, _I64, _I64, _I64, _I64, _I64]),
+    "nvfp4_kv_window_attention": (_I, [_P, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64,
+                                       _I64, _I64, ctypes.c_float, _P, _P, _P, _SZ, _P]),
 }
 _bound = None
 
@@ -159,6 +167,48 @@ def write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor)
         _stream(cache)), "nvfp4_kv_write")
 
 
+def append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor,
+           rotary: Rotary, q: torch.Tensor | None = None, *, q_out: torch.Tensor | None = None):
+    """``write`` with k turned by the tokens' positions on the way (int64 [tokens], or [axes, tokens] with
+    the rotary's axes; ``rotary.rotate`` without the rounding to k's type), v as it is. The rotary's
+    pairs are a multiple of 8. Returns q [tokens, heads, head_dim] turned too, of every token, also
+    of those that have no slot; None without q. ``q_out`` may be q itself (in place). One launch."""
+    dt, k_ts, k_hs = _rows(k, "k", cache, cache.kv_heads)
+    v_dt, v_ts, v_hs = _rows(v, "v", cache, cache.kv_heads)
+    if v_dt != dt:
+        raise TypeError(f"v must be {k.dtype}, got {v.dtype}")
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise ValueError(f"v must have {n} tokens, got {v.shape[0]}")
+    _ids(slots, "slots", cache, 1, _INT64)
+    if slots.shape[0] != n:
+        raise ValueError(f"slots must have {n} elements, got {slots.shape[0]}")
+    if rotary.pairs % 8 or 2 * rotary.pairs > cache.head_dim:
+        raise ValueError(f"the rotary's pairs must be a multiple of 8 up to {cache.head_dim // 2}, got {rotary.pairs}")
+    p_stride = _positions(positions, rotary, n, cache.device)
+    heads = q_ts = q_hs = o_ts = o_hs = 0
+    if q is not None:
+        q_dt, q_ts, q_hs = _rows(q, "q", cache, None)
+        if q_dt != dt:
+            raise TypeError(f"q must be {k.dtype}, got {q.dtype}")
+        if q.shape[0] != n:
+            raise ValueError(f"q must have {n} tokens, got {q.shape[0]}")
+        heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((n, heads, cache.head_dim), dtype=q.dtype, device=q.device)
+        elif not isinstance(q_out, torch.Tensor) or q_out.shape != q.shape or q_out.dtype != q.dtype \
+                or q_out.device != q.device:
+            raise ValueError(f"q_out must be {q.dtype} {list(q.shape)} on {q.device}")
+        _, o_ts, o_hs = _row_strides(q_out, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check((_bound or lib()).nvfp4_kv_append(
+        cache._ref, rotary._ref, positions.data_ptr(), p_stride, None if q is None else q.data_ptr(),
+        k.data_ptr(), v.data_ptr(), dt, n, heads, q_ts, q_hs, k_ts, k_hs, v_ts, v_hs,
+        None if q is None else q_out.data_ptr(), o_ts, o_hs, slots.data_ptr(), _stream(cache)), "nvfp4_kv_append")
+    return q_out
+
+
 def read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16):
     """Keys and values [n, kv_heads, head_dim] of the slots [n] (int64), dequantised to `dtype`;
     zeros for slots outside the cache."""
@@ -174,9 +224,13 @@ def read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat1
 
 
 def attention_workspace_size(cache: KVCache, dtype: torch.dtype, tokens: int, heads: int, batch: int,
-                             max_q: int, max_kv: int, prefix_len: int = 0) -> int:
+                             max_q: int, max_kv: int, prefix_len: int = 0, *, window: int | None = None,
+                             sinks: int = 0) -> int:
     """Bytes of workspace that `attention` needs for these sizes."""
     dt = nvfp4.DTYPE_BF16 if dtype == torch.bfloat16 else nvfp4.DTYPE_F32
+    if window is not None:
+        return int(lib().nvfp4_kv_window_attention_workspace_size(cache._ref, dt, tokens, heads, batch, max_q,
+                                                                  max_kv, window, sinks))
     return int(lib().nvfp4_kv_attention_workspace_size(cache._ref, dt, tokens, heads, batch, max_q,
                                                        max_kv, prefix_len))
 
@@ -185,8 +239,9 @@ def attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor | None 
               kv_lens: torch.Tensor | None = None, *, q_offsets: torch.Tensor | None = None,
               max_q: int | None = None, max_kv: int | None = None,
               prefix_pages: torch.Tensor | None = None, prefix_len: int = 0,
-              scale: float | None = None, causal: bool = True, out: torch.Tensor | None = None,
-              return_lse: bool = False, workspace: torch.Tensor | None = None):
+              scale: float | None = None, causal: bool = True, window: int | None = None, sinks: int = 0,
+              out: torch.Tensor | None = None, return_lse: bool = False,
+              workspace: torch.Tensor | None = None):
     """Softmax attention of q [tokens, heads, head_dim] (bf16 or fp32, rows may be strided) over
     cached tokens; query head j reads key/value head j // (heads // kv_heads).
 
@@ -198,6 +253,11 @@ def attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor | None 
     j <= kv_lens[b] - n + i if `causal`, all of them otherwise. max_q defaults to tokens and
     max_kv to width * page_size; smaller true bounds save work. scale defaults to
     head_dim ** -0.5.
+
+    With `window`, a query at position P = kv_lens[b] - n + i sees the tokens t <= P with t > P - window,
+    and the first `sinks` tokens up to its own. Only those are read: pages between them may be gone
+    from the block table. A window is causal and takes no prefix (a prompt that all share can stand in
+    every block table).
 
     Returns out [tokens, heads, head_dim] in q's dtype (zeros for a query that sees nothing),
     and with return_lse also lse [tokens, heads] fp32 (the logarithm of the softmax sum; -inf for
@@ -234,6 +294,13 @@ def attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor | None 
     max_kv = room if max_kv is None else min(int(max_kv), room)
     if max_q < 0 or max_kv < 0 or prefix_len < 0:
         raise ValueError("max_q, max_kv and prefix_len must not be negative")
+    if window is not None:
+        if not causal or prefix_len:
+            raise ValueError("a window is causal and takes no prefix")
+        if not 1 <= window <= MAX_WINDOW or not 0 <= sinks <= MAX_WINDOW:
+            raise ValueError(f"window must be 1 to 2^30 and sinks 0 to 2^30, got {window} and {sinks}")
+    elif sinks:
+        raise ValueError("sinks without a window")
     pages = None
     if prefix_len:
         _ids(prefix_pages, "prefix_pages", cache, 1)
@@ -246,23 +313,33 @@ def attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor | None 
         _arg(out, "out", q, q.dtype, numel=q.numel())
     lse = torch.empty(tokens, heads, dtype=torch.float32, device=q.device) if return_lse else None
     L = _bound or lib()
-    sizes = (dt, tokens, heads, batch, max_q, max_kv, prefix_len)
+    if window is None:
+        sizes, size_of = (dt, tokens, heads, batch, max_q, max_kv, prefix_len), L.nvfp4_kv_attention_workspace_size
+    else:
+        sizes = (dt, tokens, heads, batch, max_q, max_kv, window, sinks)
+        size_of = L.nvfp4_kv_window_attention_workspace_size
     need = cache._needs.get(sizes)
     if need is None:
         if len(cache._needs) >= 4096:
             cache._needs.clear()
-        need = cache._needs[sizes] = L.nvfp4_kv_attention_workspace_size(cache._ref, *sizes)
+        need = cache._needs[sizes] = size_of(cache._ref, *sizes)
     if workspace is not None:
         _arg(workspace, "workspace", cache.k_codes, torch.uint8, min_numel=need)
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check(L.nvfp4_kv_attention(
-        cache._ref, q.data_ptr(), dt, tokens, heads, q_ts, q_hs, batch,
-        None if q_offsets is None else q_offsets.data_ptr(), max_q,
-        None if block_table is None else block_table.data_ptr(), width,
-        None if kv_lens is None else kv_lens.data_ptr(), max_kv, pages, prefix_len,
-        hd ** -0.5 if scale is None else scale, int(causal), out.data_ptr(),
-        None if lse is None else lse.data_ptr(),
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), _stream(cache)), "nvfp4_kv_attention")
+    scale = hd ** -0.5 if scale is None else scale
+    offsets = None if q_offsets is None else q_offsets.data_ptr()
+    table = None if block_table is None else block_table.data_ptr()
+    lens = None if kv_lens is None else kv_lens.data_ptr()
+    ends = (out.data_ptr(), None if lse is None else lse.data_ptr(),
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel(), _stream(cache))
+    if window is None:
+        _check(L.nvfp4_kv_attention(
+            cache._ref, q.data_ptr(), dt, tokens, heads, q_ts, q_hs, batch, offsets, max_q, table, width, lens,
+            max_kv, pages, prefix_len, scale, int(causal), *ends), "nvfp4_kv_attention")
+    else:
+        _check(L.nvfp4_kv_window_attention(
+            cache._ref, q.data_ptr(), dt, tokens, heads, q_ts, q_hs, batch, offsets, max_q, table, width, lens,
+            max_kv, window, sinks, scale, *ends), "nvfp4_kv_window_attention")
     return (out, lse) if return_lse else out
