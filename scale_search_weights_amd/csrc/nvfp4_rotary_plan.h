@@ -1,0 +1,81 @@
+// How the rotation and the append are split into workgroups: host code without HIP.
+#pragma once
+
+#include <stdint.h>
+
+namespace nvfp4 {
+
+constexpr int kTable = 2048;  // cosine and sine pairs of a workgroup: 16 KiB of LDS
+constexpr int kHeads = 64;    // key/value heads a workgroup takes at most (their scales are in LDS too)
+
+// Workgroups wanted before they take more tokens each: two a CU.
+constexpr int64_t kEnough = 512;
+
+// Rows by (tokens of a workgroup, heads of a workgroup); a row is `units` items.
+struct RowPlan {
+  int units, heads;
+  int64_t groups;  // of heads
+};
+
+// `most` items a token at most; few items in all: one a lane.
+inline RowPlan heads_of(int64_t tokens, int64_t heads, int units, int64_t most, int64_t cap) {
+  if (tokens * heads * units < kEnough * 256) most = 256;
+  int64_t per = most / units;
+  per = per < 1 ? 1 : per;
+  per = per < cap ? per : cap;
+  per = per < heads ? per : heads;
+  per = per < 1 ? 1 : per;
+  return {units, (int)per, (heads + per - 1) / per};
+}
+
+// Tokens of a workgroup: so many that it has `items`, as far as its table holds them and enough
+// workgroups are left.
+inline int tokens_of(int64_t tokens, int pairs, int64_t items_a_token, int64_t items, int64_t groups) {
+  int n = 1;
+  while (2 * n * items_a_token <= items && 2 * n * pairs <= kTable && tokens / (2 * n) * groups >= kEnough) n *= 2;
+  return n;
+}
+
+struct RotatePlan {
+  int v;  // channels of a piece
+  int tokens;
+  RowPlan rows;
+};
+
+// Pieces of 16 bytes, or of 8 where the halves of bf16 rows do not begin at multiples of 16. Four tokens
+// of 32 heads of 128, bf16, 1024 items: 12000 tokens in 31.9 us with 512 items a workgroup, 31.7 with 1024,
+// 34.5 with 256; 32 tokens of 40 heads 3.2 us with an item a lane, 3.6 with two.
+inline RotatePlan rotate_plan(bool bf16, int64_t tokens, int64_t heads, int64_t head_dim, int pairs) {
+  RotatePlan p;
+  p.v = bf16 && pairs % 8 == 0 && head_dim % 16 == 0 ? 8 : 4;
+  p.rows = heads_of(tokens, heads, (int)head_dim / (2 * p.v), 1024, heads);
+  p.tokens = tokens_of(tokens, pairs, (int64_t)p.rows.heads * p.rows.units, 512, p.rows.groups);
+  return p;
+}
+
+struct AppendPlan {
+  int tokens;
+  RowPlan kv, q;  // kv for keys and for values
+};
+
+inline AppendPlan append_plan(bool bf16, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int pairs) {
+  AppendPlan p;
+  const int units = (int)head_dim / 16;
+  p.kv = heads_of(tokens, kv_heads, units, 4096, kHeads);
+  const int q_units = bf16 ? units : 2 * units;
+  const int64_t q_items = heads * q_units;
+  const int64_t groups = 2 * p.kv.groups + (q_items + 2047) / 2048;
+  p.tokens = tokens_of(tokens, pairs, (int64_t)p.kv.heads * units, heads >= 2 * kv_heads ? 256 : 512, groups);
+  p.q = heads_of(tokens, heads, q_units, 2048 / p.tokens, heads);
+  return p;
+}
+
+// f(chunks of this launch, the first one's first token), for all tokens in chunks of n: with `groups`
+// workgroups a chunk, of 256 threads, a launch stays under 2^32 threads.
+template <typename F>
+void each_chunks(int64_t tokens, int n, int64_t groups, F f) {
+  const int64_t chunks = (tokens + n - 1) / n, fit = ((1 << 24) - 1) / groups / 8 * 8, most = fit < 8 ? 8 : fit;
+  for (int64_t at = 0; at < chunks; at += most) f(chunks - at < most ? chunks - at : most, at * n);
+}
+
+}  // namespace nvfp4
