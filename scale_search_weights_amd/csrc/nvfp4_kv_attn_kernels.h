@@ -928,6 +928,45 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
   }
 }
 
+// Sixteen rows of a wave, row i of them scaled by the f of its lanes, out through LDS (32 HD bytes that no
+// other wave uses): lanes hold pieces of 4 to 16 channels of 16 rows, and stored like that every store
+// touches 64 lines (2 x 2048 queries, window 1024: 112 us, so 92). fp32 rows go eight at a time. The
+// 16-byte pieces of a row are permuted by its number, so that neither side has more than two-way bank
+// conflicts. row_at(r) is the row's first element.
+template <int HD, bool F32, typename At>
+__device__ __forceinline__ void store_tile(void *out, int hd, int rows, int r0, int lane, const f4 *acc, float f,
+                                           u4 *lds, At row_at) {
+  constexpr int DV = HD / 16, E = F32 ? 4 : 8, PIECES = HD / E, ROWS = F32 ? 8 : 16, AT_ONCE = more(64 / PIECES);
+  constexpr int MASK = PIECES < ROWS ? PIECES - 1 : ROWS - 1;
+  const int i = lane & 15, quad = lane >> 4, piece = lane % PIECES;
+#pragma unroll
+  for (int first = 0; first < 16; first += ROWS) {
+    if (ROWS == 16 || (i & 8) == first) {
+      const int row = i & (ROWS - 1);
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+#pragma unroll
+        for (int d = 0; d < DV; d += 4) {
+          const int ch = DV * (4 * quad + r4) + d;
+          const f4 y = {acc[d][r4] * f, acc[d + 1][r4] * f, acc[d + 2][r4] * f, acc[d + 3][r4] * f};
+          u4 *at = lds + row * PIECES + (ch / E ^ (row & MASK));
+          if (F32) *reinterpret_cast<f4 *>(at) = y;
+          else reinterpret_cast<u2 *>(at)[ch / 4 & 1] = (u2){bf16x2_bits(y[0], y[1]), bf16x2_bits(y[2], y[3])};
+        }
+      }
+    }
+    order_wave_lds();
+#pragma unroll
+    for (int k = 0; k < ROWS; k += AT_ONCE) {
+      const int row = k + lane / PIECES, r = r0 + first + row;
+      const u4 y = lds[row * PIECES + (piece ^ (row & MASK))];
+      if (r < rows && E * piece < hd)
+        *reinterpret_cast<u4 *>(static_cast<char *>(out) + (row_at(r) + E * piece) * (16 / E)) = y;
+    }
+    order_wave_lds();
+  }
+}
+
 // Many query rows over one token list (a shared prefix, a prompt): each of W waves holds 16 NT
 // rows. A stage is 16 W tokens: every wave dequantises a group of 16 into LDS, as ready MFMA
 // operands in lane order (bank conflicts in 3% of the cycles), and all waves read all tiles. Two stages
@@ -964,7 +1003,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   bool lead = p.lead_len > 0;
   if (lead) j.pages = p.lead, j.len = p.lead_len, j.causal = 0, t0 = 0, t1 = p.lead_len;
   const Where<WIN> gap = where_of<WIN>(p, j, R0);
-  int near = 0;  // the wave's last row's window begins here
+  int near = 0, begin = 0;  // where the window of the wave's last row begins, and of its first (as an index)
   Pages pg;
   const auto open = [&]() {
     int none;
@@ -972,7 +1011,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
     if constexpr (WIN) piece_of(p, gap, lim_hi, t0, t1);
     else t1 = min(t1, lim_hi);
     row_limits(p, j, min(r0, rows - 1), min(r0 + 16 * NT, rows), lim_lo, lim_hi);
-    if constexpr (WIN) near = lim_hi - p.window;
+    if constexpr (WIN) near = lim_hi - p.window, begin = gap.index(lim_lo - p.window);
     lim_hi = gap.index(lim_hi);
     if (r0 >= rows) lim_hi = 0;  // a wave without rows only dequantises
     pg = open_pages(j, gap, p.page_shift, t0, t1, lane);
@@ -1035,6 +1074,14 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
   #pragma unroll 1
       for (int c = 0; c < tiles; ++c) {
         const int tt = t + 32 * c;
+        if (WIN && tt >= p.sinks && tt + 32 <= begin) {  // before the windows of all of the wave's rows
+          if constexpr (AHEAD) {
+            const int nc = min(c + 1, GS / 2 - 1);
+#pragma unroll
+            for (int k = 0; k < 2 * KS; ++k) kf[k] = kfrag[b][2 * nc + k / KS][k % KS][lane];
+          }
+          continue;
+        }
         __builtin_amdgcn_s_setprio(1);
         f4 s[NT][2];
   #pragma unroll
@@ -1090,7 +1137,7 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
     if (t0 < t1) fetch(t0);
   }
 
-  // each lane holds HD/16 consecutive channels of its row four times
+  // each lane holds HD/16 consecutive channels of its row four times; no wave reads kfrag any more
   const int64_t part = part_of(p, sh);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -1098,31 +1145,21 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
     l += xor16(l);
     l += xor32(l);
     const int r = r0 + 16 * n + i;
-    if (r >= rows) continue;
-    const int tok = r / p.group, head = h * p.group + (r - tok * p.group);
-    const int64_t at = (int64_t)(j.q0 + tok) * p.heads + head;
     const float f = sh.direct ? out_factor(S_v, l) : 1.0f;
-#pragma unroll
-    for (int r4 = 0; r4 < 4; ++r4) {
-      const int ch = DV * (4 * quad + r4);
-      if (EXACT || ch < p.hd) {
-#pragma unroll
-        for (int d = 0; d < DV; d += 4) {
-          const f4 y = {x.acc[n][d][r4] * f, x.acc[n][d + 1][r4] * f, x.acc[n][d + 2][r4] * f,
-                        x.acc[n][d + 3][r4] * f};
-          if (sh.direct)
-            store4<F32>(p.out, at * p.hd + ch + d, y);
-          else
-            *reinterpret_cast<f4 *>(p.list[sh.list].opart + (part + r) * p.hd + ch + d) = y;
-        }
-      }
+    if (quad == 0 && r < rows) {
+      const int tok = r / p.group, head = h * p.group + (r - tok * p.group);
+      if (!sh.direct) p.list[sh.list].ml[part + r] = make_float2(-x.off[n], l);
+      else if (p.lse) p.lse[(int64_t)(j.q0 + tok) * p.heads + head] = row_lse(-x.off[n], l);
     }
-    if (quad == 0) {
-      if (sh.direct) {
-        if (p.lse) p.lse[at] = row_lse(-x.off[n], l);
-      } else {
-        p.list[sh.list].ml[part + r] = make_float2(-x.off[n], l);
-      }
+    u4 *lds = reinterpret_cast<u4 *>(kfrag) + wave * 2 * HD;
+    if (sh.direct) {
+      store_tile<HD, F32>(p.out, p.hd, rows, r0 + 16 * n, lane, x.acc[n], f, lds, [&](int r) {
+        const int tok = r / p.group, head = h * p.group + (r - tok * p.group);
+        return ((int64_t)(j.q0 + tok) * p.heads + head) * p.hd;
+      });
+    } else {
+      store_tile<HD, true>(p.list[sh.list].opart, p.hd, rows, r0 + 16 * n, lane, x.acc[n], f, lds,
+                           [&](int r) { return (part + r) * p.hd; });
     }
   }
 }
@@ -1143,8 +1180,11 @@ void launch_rows(const Attn &p, const Part &r, unsigned grid, hipStream_t st) {
     }
   } else if (r.waves > 4) {
     if constexpr (HD <= 128 && !F32) {
-      if (r.waves == 16) hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT, 16, WIN>), g, b, 0, st, p);
-      else hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT, 8, WIN>), g, b, 0, st, p);
+      if (r.waves == 8) {
+        hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT, 8, WIN>), g, b, 0, st, p);
+      } else if constexpr (!WIN) {  // a window's call has no use for sixteen
+        hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT, 16, WIN>), g, b, 0, st, p);
+      }
     }
   } else if (r.nt == 1) {
     hipLaunchKernelGGL((k_kv_attn_rows<HD, 1, F32, EXACT, 4, WIN>), g, b, 0, st, p);

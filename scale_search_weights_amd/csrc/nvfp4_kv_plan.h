@@ -260,35 +260,4 @@ inline size_t kv_attention_workspace_size(const KvAttention &a, const Plan &p) {
 }
 inline size_t kv_attention_workspace_size(const KvAttention &a) { return kv_attention_workspace_size(a, plan_of(a)); }
 
-// Attention over a window of each row's last tokens and the sequence's first ones. A row tile reads at
-// most `span` tokens however long the context is, so the plan is that of contexts of so many, and
-// since the spans of a batch are much the same, each is cut into the same number of pieces.
-struct WindowPlan {
-  Plan plan;
-  int pieces;
-};
-
-inline int64_t window_span(const KvAttention &a, int64_t window, int64_t sinks) {
-  const int64_t G = a.heads / a.cache->kv_heads, rows = a.max_q * G;
-  const int64_t tile = cdiv(rows < 256 ? rows : 256, G) + 1;  // tokens that a row tile holds
-  const int64_t span = cdiv(sinks, 16) * 16 + window + 15 + tile;
-  return span < a.max_kv ? span : a.max_kv;
-}
-
-inline WindowPlan window_plan_of(const KvAttention &a, int64_t window, int64_t sinks) {
-  KvAttention x = a;
-  x.max_kv = window_span(a, window, sinks);
-  WindowPlan w = {plan_of(x), 1};
-  Plan &p = w.plan;
-  if (p.own.target > 0.0f) {
-    const int64_t units = a.cache->kv_heads * p.own.row_tiles * a.batch, most = cdiv(x.max_kv, 128);
-    const int64_t n = units < p.own.resident ? p.own.resident / units : 1;
-    w.pieces = (int)(n < most ? n : most);
-  }
-  p.own.slots = (int)(a.batch * w.pieces);
-  p.own.target = w.pieces > 1 ? (float)p.own.slots : 0.0f;
-  p.direct = w.pieces == 1;
-  return w;
-}
-
 }  // namespace nvfp4

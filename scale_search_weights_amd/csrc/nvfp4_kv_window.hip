@@ -5,6 +5,7 @@
 // row tile reads the sinks' groups of 16 tokens, then those that its rows' windows cover, so the work
 // is that of sinks + window tokens however long the context is.
 #include "nvfp4_kv_attn_kernels.h"
+#include "nvfp4_kv_window_plan.h"
 
 namespace nvfp4 {
 

@@ -1,5 +1,6 @@
 // C-ABI entry points of windowed attention over the key/value cache (declared in include/nvfp4_kv.h).
 #include "nvfp4_kv_checks.h"
+#include "nvfp4_kv_window_plan.h"
 
 using namespace nvfp4;
 
