@@ -72,7 +72,6 @@ inline double tile_time(const TileCost &c, double k, double steps) {
 inline WindowPlan window_tile_plan(const KvAttention &a, int64_t window, int64_t sinks) {
   WindowPlan best = {};
   double least = INFINITY;
-  best.pieces = 1;
   const bool wide = a.cache->head_dim > 128, f32 = a.dtype == NVFP4_DTYPE_F32;
   const int64_t G = a.heads / a.cache->kv_heads, rows = a.max_q * G, units = a.batch * a.cache->kv_heads;
   for (int kind = 0; kind < 3; ++kind) {
@@ -81,9 +80,9 @@ inline WindowPlan window_tile_plan(const KvAttention &a, int64_t window, int64_t
     const int64_t tile = 16 * nt * waves, row_tiles = cdiv(rows, tile);
     const int64_t span = window_span(a, window, sinks, tile < rows ? tile : rows);
     const TileCost c = tile_cost(nt, waves, a.cache->head_dim, f32);
-    const int64_t blocks = cdiv(span, 128);
+    const int64_t blocks = cdiv(span > 0 ? span : 1, 128);
     for (int64_t per = blocks; per > 0; per = per > 16 ? per / 2 : per - 1) {  // blocks of 128 tokens a piece
-      const int64_t pieces = cdiv(blocks, per < 1 ? 1 : per);
+      const int64_t pieces = cdiv(blocks, per);
       if (pieces > 1 && units * row_tiles * pieces > 4 * kCus) break;
       double us = tile_time(c, (double)cdiv(units * row_tiles * pieces, kCus), (double)(2 * per));
       if (pieces > 1) us += 5.0 + 0.3e-6 * (double)(a.batch * pieces * rows * a.cache->kv_heads * a.cache->head_dim * 4);

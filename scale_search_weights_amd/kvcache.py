@@ -15,6 +15,7 @@ no CPU fallback, and no gradient flows through the results.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 import torch
 
@@ -183,9 +184,9 @@ def append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor
     _ids(slots, "slots", cache, 1, _INT64)
     if slots.shape[0] != n:
         raise ValueError(f"slots must have {n} elements, got {slots.shape[0]}")
+    p_stride = _positions(positions, rotary, n, cache.device)
     if rotary.pairs % 8 or 2 * rotary.pairs > cache.head_dim:
         raise ValueError(f"the rotary's pairs must be a multiple of 8 up to {cache.head_dim // 2}, got {rotary.pairs}")
-    p_stride = _positions(positions, rotary, n, cache.device)
     heads = q_ts = q_hs = o_ts = o_hs = 0
     if q is not None:
         q_dt, q_ts, q_hs = _rows(q, "q", cache, None)
@@ -297,6 +298,7 @@ def attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor | None 
     if window is not None:
         if not causal or prefix_len:
             raise ValueError("a window is causal and takes no prefix")
+        window, sinks = operator.index(window), operator.index(sinks)
         if not 1 <= window <= MAX_WINDOW or not 0 <= sinks <= MAX_WINDOW:
             raise ValueError(f"window must be 1 to 2^30 and sinks 0 to 2^30, got {window} and {sinks}")
     elif sinks:

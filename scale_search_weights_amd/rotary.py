@@ -115,6 +115,8 @@ def _stream(device: torch.device) -> int:
 
 def _positions(positions, rotary: Rotary, tokens: int, device: torch.device) -> int:
     """Checks int64 positions [tokens] (one axis) or [axes, tokens]; returns the axes' stride."""
+    if not isinstance(rotary, Rotary):
+        raise TypeError("rotary must be a Rotary")
     if not isinstance(positions, torch.Tensor):
         raise TypeError("positions must be a torch tensor")
     if positions.device != device or rotary.device != device:
@@ -152,9 +154,9 @@ def _row_strides(t, name: str):
 def _launch(x, positions, rotary: Rotary, transpose: bool, out):
     dt, ts, hs = _row_strides(x, "x")
     tokens, heads, hd = x.shape
+    stride = _positions(positions, rotary, tokens, x.device)
     if hd % 8 or hd < 2 * rotary.pairs or hd > MAX_HEAD_DIM:
         raise ValueError(f"head_dim must be a multiple of 8 from {2 * rotary.pairs} to {MAX_HEAD_DIM}, got {hd}")
-    stride = _positions(positions, rotary, tokens, x.device)
     if out is None:
         out = torch.empty((tokens, heads, hd), dtype=x.dtype, device=x.device)
     elif not isinstance(out, torch.Tensor) or out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
