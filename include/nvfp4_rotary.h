@@ -35,8 +35,8 @@ typedef struct nvfp4_rotary {
   const double *inv_freq;
   const int32_t *axis;
   int64_t pairs, axes;
+  double factor;
   int adjacent;
-  float factor;
 } nvfp4_rotary;
 
 /*

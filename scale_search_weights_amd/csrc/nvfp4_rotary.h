@@ -20,8 +20,8 @@ struct Turn {
   const int32_t *axis;
   const int64_t *positions;
   int64_t stride;
+  double factor;
   int pairs, axes;
-  float factor;
 };
 
 int launch_rotate(const Turn &turn, bool adjacent, bool transpose, const RowSpan &x,

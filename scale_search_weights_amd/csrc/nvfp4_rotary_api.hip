@@ -23,7 +23,7 @@ int check_positions(const nvfp4_rotary *r, const int64_t *positions, int64_t str
   if (!r->inv_freq || !positions) return NVFP4_ERR_NULL;
   if (!aligned(r->inv_freq, 8) || !aligned(r->axis, 4) || !aligned(positions, 8)) return NVFP4_ERR_ALIGN;
   if (stride < 0 || stride > INT64_MAX / 256 || tokens > INT64_MAX / 256) return NVFP4_ERR_SHAPE;
-  *turn = {r->inv_freq, r->axis, positions, stride, (int)r->pairs, (int)r->axes, r->factor};
+  *turn = {r->inv_freq, r->axis, positions, stride, r->factor, (int)r->pairs, (int)r->axes};
   return NVFP4_OK;
 }
 

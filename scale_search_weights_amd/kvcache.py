@@ -21,7 +21,7 @@ import torch
 
 from . import nvfp4
 from .nvfp4 import _I, _I64, _P, _SZ, _arg, _check, _dt, _need
-from .rotary import Rotary, _positions, _row_strides
+from .rotary import Rotary, _given_out, _positions
 
 MAX_HEAD_DIM = 1024            # write, read
 MAX_ATTENTION_HEAD_DIM = 256
@@ -197,10 +197,9 @@ def append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor
         heads = q.shape[1]
         if q_out is None:
             q_out = torch.empty((n, heads, cache.head_dim), dtype=q.dtype, device=q.device)
-        elif not isinstance(q_out, torch.Tensor) or q_out.shape != q.shape or q_out.dtype != q.dtype \
-                or q_out.device != q.device:
-            raise ValueError(f"q_out must be {q.dtype} {list(q.shape)} on {q.device}")
-        _, o_ts, o_hs = _row_strides(q_out, "q_out")
+            o_ts, o_hs = heads * cache.head_dim, cache.head_dim
+        else:
+            o_ts, o_hs = _given_out(q_out, "q_out", q)
     elif q_out is not None:
         raise ValueError("q_out without q")
     _check((_bound or lib()).nvfp4_kv_append(

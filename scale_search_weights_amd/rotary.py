@@ -28,8 +28,8 @@ MAX_AXES = 16
 
 
 class _Rotary(ctypes.Structure):
-    _fields_ = [("inv_freq", _P), ("axis", _P), ("pairs", _I64), ("axes", _I64), ("adjacent", _I),
-                ("factor", ctypes.c_float)]
+    _fields_ = [("inv_freq", _P), ("axis", _P), ("pairs", _I64), ("axes", _I64), ("factor", ctypes.c_double),
+                ("adjacent", _I)]
 
 
 _SIGS = {
@@ -64,6 +64,8 @@ class Rotary:
         _need(inv_freq, "inv_freq")
         if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
             raise TypeError("inv_freq must be torch.float64 with 1 dimension")
+        if inv_freq.requires_grad:
+            raise ValueError("no gradient flows to inv_freq")
         pairs = inv_freq.shape[0]
         if pairs < 4 or pairs % 4 or pairs > MAX_PAIRS:
             raise ValueError(f"the pairs must be a multiple of 4 up to {MAX_PAIRS}, got {pairs}")
@@ -83,7 +85,7 @@ class Rotary:
         self.adjacent, self.factor, self.device = bool(adjacent), float(factor), inv_freq.device
         self._index = self.device.index
         self._c = _Rotary(inv_freq.data_ptr(), None if axis is None else axis.data_ptr(), pairs, axes,
-                          int(self.adjacent), self.factor)
+                          self.factor, int(self.adjacent))
         self._ref = ctypes.addressof(self._c)
 
     @classmethod
@@ -151,7 +153,19 @@ def _row_strides(t, name: str):
     return dt, ts, hs
 
 
-def _launch(x, positions, rotary: Rotary, transpose: bool, out):
+def _given_out(out, name: str, like):
+    """Strides of an output that the caller gives, with like's shape and type; what autograd saved of it before
+    counts as changed from here on."""
+    if not isinstance(out, torch.Tensor) or out.shape != like.shape or out.dtype != like.dtype \
+            or out.device != like.device:
+        raise ValueError(f"{name} must be {like.dtype} {list(like.shape)} on {like.device}")
+    _, ts, hs = _row_strides(out, name)
+    if not out.is_inference():
+        torch.autograd.graph.increment_version(out)
+    return ts, hs
+
+
+def _launch(x, positions, rotary: Rotary, transpose: bool, out=None):
     dt, ts, hs = _row_strides(x, "x")
     tokens, heads, hd = x.shape
     stride = _positions(positions, rotary, tokens, x.device)
@@ -159,9 +173,9 @@ def _launch(x, positions, rotary: Rotary, transpose: bool, out):
         raise ValueError(f"head_dim must be a multiple of 8 from {2 * rotary.pairs} to {MAX_HEAD_DIM}, got {hd}")
     if out is None:
         out = torch.empty((tokens, heads, hd), dtype=x.dtype, device=x.device)
-    elif not isinstance(out, torch.Tensor) or out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
-        raise ValueError(f"out must be {x.dtype} {list(x.shape)} on {x.device}")
-    _, ots, ohs = _row_strides(out, "out")
+        ots, ohs = heads * hd, hd
+    else:
+        ots, ohs = _given_out(out, "out", x)
     _check((_bound or lib()).nvfp4_rotate(
         rotary._ref, positions.data_ptr(), stride, x.data_ptr(), dt, tokens, heads, hd, ts, hs,
         out.data_ptr(), ots, ohs, int(transpose), _stream(x.device)), "nvfp4_rotate")
@@ -170,24 +184,31 @@ def _launch(x, positions, rotary: Rotary, transpose: bool, out):
 
 def _aligned(g):
     """The gradient itself where the kernel can read it, else a contiguous copy (an expanded one, say)."""
-    ok = g.stride(2) == 1 and not g.data_ptr() & 15 and all(
-        n <= 1 or s * g.element_size() % 16 == 0 for n, s in zip(g.shape[:2], g.stride()[:2]))
-    return g if ok else g.contiguous()
+    ts, hs, ds = g.stride()
+    if ds == 1 and not (g.data_ptr() | (ts | hs) * g.element_size()) & 15:
+        return g
+    return g.clone(memory_format=torch.contiguous_format)
 
 
 class _Turned(torch.autograd.Function):
-    """y = R x; dx = R^T dy, which is differentiable in turn."""
+    """y = R x; dx = R^T dy, which is differentiable in turn. The tensors that make R are inputs so that they
+    can be saved: a backward pass after one of them was changed is refused."""
 
     @staticmethod
-    def forward(ctx, x, positions, rotary, transpose):
-        ctx.save_for_backward(positions, rotary.inv_freq, rotary.axis)  # refuses if they change meanwhile
+    def forward(ctx, x, positions, inv_freq, axis, rotary, transpose):
+        ctx.save_for_backward(positions, inv_freq, axis)
         ctx.rotary, ctx.transpose = rotary, transpose
-        return _launch(x, positions, rotary, transpose, None)
+        return _launch(x, positions, rotary, transpose)
 
     @staticmethod
     def backward(ctx, gy):
         positions = ctx.saved_tensors[0]
-        return _Turned.apply(_aligned(gy), positions, ctx.rotary, not ctx.transpose), None, None, None
+        turn = _turned if torch.is_grad_enabled() else _launch
+        return turn(_aligned(gy), positions, ctx.rotary, not ctx.transpose), None, None, None, None, None
+
+
+def _turned(x, positions, rotary: Rotary, transpose: bool):
+    return _Turned.apply(x, positions, rotary.inv_freq, rotary.axis, rotary, transpose)
 
 
 def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, *, transpose: bool = False,
@@ -196,9 +217,10 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, *, transpos
     (int64 [tokens], or [axes, tokens] with the rotary's axes). head_dim is a multiple of 8, at least
     2 * rotary.pairs. Queries and keys that lie beside each other in a fused projection can be turned
     in one call. With ``transpose`` the transposed matrix (for factor 1 the turn back). ``out`` may be x
-    itself (in place), and is then not differentiable; otherwise gradients flow to x."""
+    itself (in place); without it gradients flow to x. As with any operator, a backward pass that is captured
+    into a graph needs leaves that no eager graph still holds."""
     if torch.is_grad_enabled() and isinstance(x, torch.Tensor) and x.requires_grad:
         if out is not None:
             raise ValueError("a call that needs gradients takes no out")
-        return _Turned.apply(x, positions, rotary, transpose)
+        return _turned(x, positions, rotary, transpose)
     return _launch(x, positions, rotary, transpose, out)

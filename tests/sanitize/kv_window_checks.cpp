@@ -28,7 +28,7 @@ int main() {
   // every size of rotary and cache at its extremes; a call that passes the checks has no tokens
   for (int64_t pairs : big)
     for (int64_t axes : big) {
-      nvfp4_rotary r = {freq, ids, pairs, axes, 1, 1.0f};
+      nvfp4_rotary r = {freq, ids, pairs, axes, 1.0, 1};
       for (int64_t hd : big) {
         nvfp4_rotate(&r, pos, 0, F, 1, 0, 4, hd, 0, 0, F, 0, 0, 0, nullptr);
         nvfp4_rotate(&r, pos, axes, F, 0, 4, 0, hd, pairs, axes, F, pairs, axes, 1, nullptr);
@@ -38,7 +38,7 @@ int main() {
         }
       }
     }
-  nvfp4_rotary r = {freq, nullptr, 32, 1, 0, 1.0f};
+  nvfp4_rotary r = {freq, nullptr, 32, 1, 1.0, 0};
   nvfp4_kv_cache c = {F, F, F, F, S, S, 8, 16, 2, 64};
   for (int64_t a : big)
     for (int64_t b : big) {

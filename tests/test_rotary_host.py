@@ -20,7 +20,7 @@ def L():
 
 
 def R(inv_freq=FAKE, axis=None, pairs=32, axes=1, adjacent=0, factor=1.0):
-    return ctypes.byref(rotary._Rotary(inv_freq, axis, pairs, axes, adjacent, factor))
+    return ctypes.byref(rotary._Rotary(inv_freq, axis, pairs, axes, factor, adjacent))
 
 
 def test_exports_what_the_header_declares(L):
@@ -144,6 +144,7 @@ def _bad_calls():
         ("frequencies fp32", lambda: rotary.Rotary(G(32)), TypeError),
         ("frequencies on the host", lambda: rotary.Rotary(torch.zeros(32, dtype=f64)), ValueError),
         ("frequencies of two dimensions", lambda: rotary.Rotary(G(4, 8, dtype=f64)), TypeError),
+        ("frequencies to be trained", lambda: rotary.Rotary(G(32, dtype=f64).requires_grad_()), ValueError),
         ("30 pairs", lambda: rot(30), ValueError),
         ("516 pairs", lambda: rot(516), ValueError),
         ("axis of other length", lambda: rot(32, G(31, dtype=i32)), TypeError),
