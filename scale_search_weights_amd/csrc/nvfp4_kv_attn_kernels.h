@@ -18,7 +18,7 @@
 // memory: k_kv_attn_rows, every wave dequantising its own tokens in registers (about 260 vector
 // instructions for 32 tokens and 16 rows; 524000 tokens of 8 heads of 128, 604 MB, in 117 us,
 // 5.2 TB/s). With more rows the products bound it: k_kv_attn_tile, where the waves share what they
-// dequantise through LDS (2 x 2048 queries of 32 heads on 8192 tokens, 481 GFLOP, in 433 us,
+// dequantise through LDS (2 x 2048 queries of 32 heads on 8192 tokens, 481 GFLOP, in 426 us,
 // 1.1 PFLOP/s). The sequence axis is cut into pieces where there are few rows; their sums are
 // joined in a fixed order, by k_kv_attn_join or, where only a prefix is cut, by the workgroups of
 // the sequences' own tokens (finish_rows).

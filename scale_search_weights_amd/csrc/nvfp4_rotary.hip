@@ -1,7 +1,13 @@
 // Rotary positions, and the append to the key/value cache that turns keys on the way.
 //
-// A workgroup takes a few tokens: it computes their cosines and sines once, in 64 bits, into a table in
-// LDS, and goes over the rows of its heads in the order of memory.
+// Both are bound by memory: a turned value is read and written once, and its cosine and sine are shared by
+// all heads. A workgroup takes a few tokens: it computes their cosines and sines once, in 64 bits, into a
+// table in LDS, and goes over the rows of its heads in the order of memory. (With a lane per token and pair
+// group that goes over the heads, without a table, 12000 tokens of 32 heads of 128 took 40 us, 31 so: 6.3 TB/s,
+// over a copy's 5.1 since half of the input of two such calls in turn stays in the last cache; 9801 x 16 fp32
+// heads of 72, 90 MB, 17 us, 5.3 TB/s.) The append adds the quantiser, about 260 vector instructions a
+// block of 16, and runs at 5.4 TB/s with queries (16384 tokens of 32 and 8 heads of 128: 65 us); without
+// them vector work bounds it (27 us, 21 for the write without rotation).
 #include <type_traits>
 
 #include "nvfp4_device.h"
@@ -258,8 +264,9 @@ static Items items_of(int n, const RowPlan &r, int64_t heads) {
 }
 
 // f(adjacent, stream) with both as types. Rows are stored non-temporally where they pass the dies' L2, 32 MB in
-// all (12000 tokens of 32 heads of 128: 31.9 us, 34.5 with ordinary stores); fewer are left for whoever
-// reads them next.
+// all; fewer are left for whoever reads them next. us, non-temporal and ordinary, 32 bf16 heads of 128, three
+// inputs in turn: 16 MB 6.3, 6.7; 32 11.7, 11.6; 64 20.9, 22.8; 128 46.8, 41.2 (the ordinary ones find half of
+// it in the last cache); 256 92.4, 97.7. The append of 16384 tokens of 32 and 8 heads: 66, 69.
 template <typename F>
 static void with_flags(bool adjacent, int64_t bytes, F f) {
   const bool stream = bytes > (32 << 20);
@@ -390,8 +397,9 @@ __device__ __forceinline__ void append_items(const Append &p, const Items &it, i
 
 // The roles of a chunk of tokens (groups of key heads, of value heads, of query heads) follow each other on
 // one die: workgroups go to the 8 dies in turn. So those that quantise run beside those that only move
-// queries (16384 tokens of 32 and 8 heads of 128: 66 us, 75 with one role after the other). Six
-// workgroups a CU, 80 registers: 66 us, 71 with as many registers as it asks for, 83 with 64.
+// queries (16384 tokens of 32 and 8 heads of 128: 66 us, 74 with one role after the other). Six
+// workgroups a CU, 80 registers: 66 us, 68 with as many registers as it asks for, 83 with 64 (one role
+// after the other); fp32 needs 96.
 template <int DT, bool ADJACENT, bool STREAM>
 __global__ void __launch_bounds__(256, DT == NVFP4_DTYPE_F32 ? 5 : 6) k_kv_append(Append p, Items kv, Items q, int64_t tokens, int q_heads) {
   __shared__ __align__(16) float2 table[kTable + kTable / 8];
