@@ -290,10 +290,18 @@ struct Group {
 
 // Scales are loaded as whole words, so that nothing is done to them before they are used (a
 // narrow load's zero extension would wait for it at once). Part q of a token's four: the
-// lane's HD/64 bytes, moved down.
+// lane's HD/64 bytes, moved down. Rows of nb < HD / 16 blocks: the word begins with the lane's first byte, at
+// any address, or, at the end of the group, earlier (scale_word); bytes behind the row are another's, and
+// finite as every scale is: they meet channels that are zero in the query or are not stored.
+__device__ __forceinline__ unsigned scale_word(unsigned first, unsigned nb) { return min(first, 16 * nb - 4); }
+
 template <int HD, bool EXACT>
-__device__ __forceinline__ unsigned scale_bits(unsigned w, unsigned q) {
-  if (!EXACT || HD > 128) return w;
+__device__ __forceinline__ unsigned scale_bits(unsigned w, unsigned row, unsigned q, unsigned nb) {
+  if (!EXACT) {
+    const unsigned first = row * nb + q * (HD / 64);
+    return w >> 8 * min(first - scale_word(first, nb), 3u);
+  }
+  if (HD > 128) return w;
   return HD == 128 ? w >> 16 * (q & 1) : w >> 8 * q;
 }
 
@@ -373,15 +381,11 @@ __device__ __forceinline__ int load_group(const Attn &p, int id, int h, int t, i
       const unsigned kso = lane_offset(i * nb + (HD == 128 ? kq * 2 : kq));
       x.ks = *(const GLOBAL unsigned *)(ks + kso);
     } else {
-      x.ks = 0;
+      typedef unsigned Word __attribute__((aligned(1)));
+      x.ks = *(const GLOBAL Word *)(ks + lane_offset(scale_word(i * nb + quad * (HD / 64), nb)));
 #pragma unroll
       for (unsigned w = 0; w < HD / 64; ++w) {
-        const unsigned b = quad * (HD / 64) + w;
-        u2 a = (u2){0, 0};
-        if (b < nb) {
-          a = *(const GLOBAL u2 *)(kc + (i * nb + b) * 8);
-          x.ks |= (unsigned)ks[i * nb + b] << (8 * w);
-        }
+        const u2 a = *(const GLOBAL u2 *)(kc + lane_offset(min(i * nb + quad * (HD / 64) + w, 16 * nb - 1) * 8));
         x.k[2 * w] = a.x, x.k[2 * w + 1] = a.y;
       }
     }
@@ -391,27 +395,20 @@ __device__ __forceinline__ int load_group(const Attn &p, int id, int h, int t, i
       const unsigned vso = lane_offset((l >> 2) * nb + (HD == 128 ? vq * 2 : vq));
       x.vs = *(const GLOBAL unsigned *)(vs + vso);
     } else {
-      x.vs = 0;
-#pragma unroll
-      for (unsigned w = 0; w < HD / 64; ++w) {
-        const unsigned c = (l & 3) * (HD / 64) + w;
-        if (c < nb) x.vs |= (unsigned)vs[(l >> 2) * nb + c] << (8 * w);
-      }
+      typedef unsigned Word __attribute__((aligned(1)));
+      x.vs = *(const GLOBAL Word *)(vs + lane_offset(scale_word((l >> 2) * nb + (l & 3) * (HD / 64), nb)));
     }
-    const bool in = EXACT || (int)(i * (HD / 16)) < p.hd;
-    const unsigned vo = lane_offset(4 * quad * (nb * 8) + i * (HD / 32));
+    // channels behind the row: its last ones again
+    const unsigned c = EXACT ? i : min(i, (unsigned)p.hd / (HD / 16) - 1);
+    const unsigned vo = lane_offset(4 * quad * (nb * 8) + c * (HD / 32));
 #pragma unroll
     for (unsigned e = 0; e < 4; ++e) {
       const Bytes v = vc + e * (nb * 8);
-      x.v[e][0] = 0;
-      if constexpr (HD > 128) x.v[e][1] = 0;
-      if (in) {
-        if constexpr (HD == 64) x.v[e][0] = *(const GLOBAL uint16_t *)(v + vo);
-        else if constexpr (HD == 128) x.v[e][0] = *(const GLOBAL unsigned *)(v + vo);
-        else {
-          const u2 a = *(const GLOBAL u2 *)(v + vo);
-          x.v[e][0] = a.x, x.v[e][1] = a.y;
-        }
+      if constexpr (HD == 64) x.v[e][0] = *(const GLOBAL uint16_t *)(v + vo);
+      else if constexpr (HD == 128) x.v[e][0] = *(const GLOBAL unsigned *)(v + vo);
+      else {
+        const u2 a = *(const GLOBAL u2 *)(v + vo);
+        x.v[e][0] = a.x, x.v[e][1] = a.y;
       }
     }
   }
@@ -420,10 +417,10 @@ __device__ __forceinline__ int load_group(const Attn &p, int id, int h, int t, i
 
 // Key operands of a group: out[s] holds eight channels of the lane's token, contraction step s.
 template <int HD, bool EXACT>
-__device__ __forceinline__ void key_frags(const Group<HD> &x, int lane, h8 *out) {
+__device__ __forceinline__ void key_frags(const Group<HD> &x, int lane, unsigned nb, h8 *out) {
   h2 sc[more(HD / 128)];
 #pragma unroll
-  for (int k = 0; k < more(HD / 128); ++k) sc[k] = scales2(scale_bits<HD, EXACT>(x.ks, lane >> 4), k);
+  for (int k = 0; k < more(HD / 128); ++k) sc[k] = scales2(scale_bits<HD, EXACT>(x.ks, lane & 15, lane >> 4, nb), k);
 #pragma unroll
   for (int s = 0; s < HD / 32; ++s) {
     const _Float16 f = (s >> 1) & 1 ? sc[s >> 2][1] : sc[s >> 2][0];
@@ -440,11 +437,11 @@ __device__ __forceinline__ void key_frags(const Group<HD> &x, int lane, h8 *out)
 constexpr int kVsRow = 20;
 
 template <int HD, bool EXACT>
-__device__ __forceinline__ void stage_value_scales(const Group<HD> &x, int lane, _Float16 *lds) {
+__device__ __forceinline__ void stage_value_scales(const Group<HD> &x, int lane, unsigned nb, _Float16 *lds) {
   const int tok = lane >> 2, b0 = (lane & 3) * (HD / 64);
 #pragma unroll
   for (int w = 0; w < more(HD / 128); ++w) {
-    const h2 s = scales2(scale_bits<HD, EXACT>(x.vs, lane & 3), w);
+    const h2 s = scales2(scale_bits<HD, EXACT>(x.vs, lane >> 2, lane & 3, nb), w);
     lds[(b0 + 2 * w) * kVsRow + tok] = s[0];
     if (HD > 64) lds[(b0 + 2 * w + 1) * kVsRow + tok] = s[1];
   }
@@ -817,9 +814,9 @@ __global__ void __launch_bounds__(64 * W, NT == 1 && HD <= 128 && !F32 ? 4 : 1) 
     f4 s[NT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      stage_value_scales<HD, EXACT>(g[u], lane, vs_lds[wave][u]);
+      stage_value_scales<HD, EXACT>(g[u], lane, p.hd >> 4, vs_lds[wave][u]);
       h8 kf[HD / 32];
-      key_frags<HD, EXACT>(g[u], lane, kf);
+      key_frags<HD, EXACT>(g[u], lane, p.hd >> 4, kf);
 #pragma unroll
       for (int n = 0; n < NT; ++n) s[n][u] = (f4){0, 0, 0, 0};
 #pragma unroll
@@ -1025,11 +1022,11 @@ __global__ void __launch_bounds__(64 * W, 2) k_kv_attn_tile(Attn p) {
     ok = load_group<HD, EXACT>(p, page_of(pg, t), h, gap.token(t), lane, g, part_kv);
   };
   const auto dequantise = [&](int b) {
-    if (part_kv & 2) stage_value_scales<HD, EXACT>(g, lane, vs_lds[mine]);
+    if (part_kv & 2) stage_value_scales<HD, EXACT>(g, lane, p.hd >> 4, vs_lds[mine]);
     if (part_kv & 1) {
       if (lane == 0) oks[b][mine] = ok;
       h8 kf[KS];
-      key_frags<HD, EXACT>(g, lane, kf);
+      key_frags<HD, EXACT>(g, lane, p.hd >> 4, kf);
 #pragma unroll
       for (int k = 0; k < KS; ++k) kfrag[b][mine][k][lane] = kf[k];
     }
