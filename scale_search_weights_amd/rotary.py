@@ -18,6 +18,7 @@ import ctypes
 import math
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import nvfp4
 from .nvfp4 import _I, _I64, _P, _check, _dt, _need
@@ -165,6 +166,11 @@ def _given_out(out, name: str, like):
     return ts, hs
 
 
+def _followed(t: torch.Tensor) -> bool:
+    """Whether autograd follows t: backwards, or forwards by a tangent (in whatever mode)."""
+    return t.requires_grad and torch.is_grad_enabled() or unpack_dual(t).tangent is not None
+
+
 def _launch(x, positions, rotary: Rotary, transpose: bool, out=None):
     dt, ts, hs = _row_strides(x, "x")
     tokens, heads, hd = x.shape
@@ -192,7 +198,8 @@ def _aligned(g):
 
 class _Turned(torch.autograd.Function):
     """y = R x; dx = R^T dy, which is differentiable in turn. The tensors that make R are inputs so that they
-    can be saved: a backward pass after one of them was changed is refused."""
+    can be saved: a backward pass after one of them was changed is refused. Forward mode is not offered:
+    torch refuses a tangent here."""
 
     @staticmethod
     def forward(ctx, x, positions, inv_freq, axis, rotary, transpose):
@@ -203,7 +210,7 @@ class _Turned(torch.autograd.Function):
     @staticmethod
     def backward(ctx, gy):
         positions = ctx.saved_tensors[0]
-        turn = _turned if torch.is_grad_enabled() else _launch
+        turn = _turned if _followed(gy) else _launch
         return turn(_aligned(gy), positions, ctx.rotary, not ctx.transpose), None, None, None, None, None
 
 
@@ -217,9 +224,10 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, *, transpos
     (int64 [tokens], or [axes, tokens] with the rotary's axes). head_dim is a multiple of 8, at least
     2 * rotary.pairs. Queries and keys that lie beside each other in a fused projection can be turned
     in one call. With ``transpose`` the transposed matrix (for factor 1 the turn back). ``out`` may be x
-    itself (in place); without it gradients flow to x. As with any operator, a backward pass that is captured
-    into a graph needs leaves that no eager graph still holds."""
-    if torch.is_grad_enabled() and isinstance(x, torch.Tensor) and x.requires_grad:
+    itself (in place); without it gradients flow to x, backwards only: a tangent of forward mode is refused.
+    As with any operator, a backward pass that is captured into a graph needs leaves that no eager graph
+    still holds."""
+    if isinstance(x, torch.Tensor) and _followed(x):
         if out is not None:
             raise ValueError("a call that needs gradients takes no out")
         return _turned(x, positions, rotary, transpose)

@@ -1,0 +1,65 @@
+"""What autograd is told of the rotation: the host path of ``rotate`` with its launch replaced by a plain one (no
+GPU needed; test_gpu_rotary.py has the gradients' values)."""
+import pytest
+import torch
+import torch.autograd.forward_ad as forward_ad
+
+import rotary_ref as ref
+from scale_search_weights_amd import rotary
+from test_abi import G
+
+
+@pytest.fixture
+def plain(monkeypatch):
+    """The launch on the CPU, at the frequencies and axes of the Rotary it is given."""
+    def launch(x, positions, rot, transpose, out=None):
+        turn = ref.turns(positions.as_subclass(torch.Tensor), rot.inv_freq.as_subclass(torch.Tensor), rot.axis, rot.axes)
+        with torch.no_grad():
+            y = ref.rounded(x.as_subclass(torch.Tensor), turn, rot.adjacent, rot.factor, transpose).to(x.dtype)
+            return y if out is None else out.copy_(y)
+    monkeypatch.setattr(rotary, "_launch", launch)
+
+
+def make(tokens=5, heads=2, hd=16):
+    gen = torch.Generator().manual_seed(1)
+    x = torch.randn(tokens, heads, hd, generator=gen)
+    pos = torch.randint(0, 1000, (tokens,), generator=gen).as_subclass(type(G(1)))
+    w = G(hd // 2, dtype=torch.float64)
+    w += 10.0 ** -torch.arange(hd // 2, dtype=torch.float64)
+    return x, pos, rotary.Rotary(w)
+
+
+@pytest.mark.parametrize("grad", [True, False], ids=["gradient mode", "no_grad"])
+def test_a_tangent_is_refused_not_dropped(plain, grad):
+    """Forward mode is not offered; torch says so, also of a primal that needs no gradient."""
+    x, pos, rot = make()
+    with forward_ad.dual_level(), torch.set_grad_enabled(grad):
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        with pytest.raises(NotImplementedError):
+            rotary.rotate(dual, pos, rot)
+        with pytest.raises(ValueError):
+            rotary.rotate(dual, pos, rot, out=torch.empty_like(x))
+        y = rotary.rotate(x, pos, rot)  # nothing to follow
+        assert forward_ad.unpack_dual(y).tangent is None and torch.equal(y, rotary.rotate(x, pos, rot))
+
+
+def test_a_tangent_of_the_gradient_is_refused_not_dropped(plain):
+    x, pos, rot = make()
+    y = rotary.rotate(x.requires_grad_(), pos, rot)
+    with forward_ad.dual_level():
+        g = forward_ad.make_dual(torch.ones_like(x), torch.ones_like(x))
+        with pytest.raises(NotImplementedError):
+            torch.autograd.grad(y, x, g)
+
+
+def test_second_order(plain):
+    """The gradient is followed where its own input is, and only there."""
+    x, pos, rot = make()
+    y = rotary.rotate(x.requires_grad_(), pos, rot)
+    v, u = torch.randn_like(x).requires_grad_(), torch.randn_like(x)
+    gx, = torch.autograd.grad(y, x, v, create_graph=True)
+    gv, = torch.autograd.grad(gx, v, u)
+    assert torch.equal(gv, rotary.rotate(u, pos, rot))
+    y = rotary.rotate(x, pos, rot)
+    gx, = torch.autograd.grad(y, x, u, create_graph=True)
+    assert not gx.requires_grad and torch.equal(gx, rotary.rotate(u, pos, rot, transpose=True))
