@@ -173,7 +173,8 @@ def append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor
     """``write`` with k turned by the tokens' positions on the way (int64 [tokens], or [axes, tokens] with
     the rotary's axes; ``rotary.rotate`` without the rounding to k's type), v as it is. The rotary's
     pairs are a multiple of 8. Returns q [tokens, heads, head_dim] turned too, of every token, also
-    of those that have no slot; None without q. ``q_out`` may be q itself (in place). One launch."""
+    of those that have no slot; None without q. ``q_out`` may be q itself (in place); one that autograd follows
+    (q of a projection that is being trained) is refused outside of torch.no_grad(). One launch."""
     dt, k_ts, k_hs = _rows(k, "k", cache, cache.kv_heads)
     v_dt, v_ts, v_hs = _rows(v, "v", cache, cache.kv_heads)
     if v_dt != dt:

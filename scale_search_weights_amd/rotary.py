@@ -154,21 +154,29 @@ def _row_strides(t, name: str):
     return dt, ts, hs
 
 
+def _followed(t: torch.Tensor) -> bool:
+    """Whether autograd follows t: backwards, or forwards by a tangent (in whatever mode)."""
+    return t.requires_grad and torch.is_grad_enabled() or unpack_dual(t).tangent is not None
+
+
+def _overwritten(t: torch.Tensor, name: str) -> None:
+    """A tensor of the caller's is about to be written by a kernel. One that autograd follows would keep the
+    history of what it held before, and is refused; what autograd saved of it counts as changed from here on."""
+    if _followed(t):
+        raise ValueError(f"{name} is followed by autograd and no gradient would flow to it: detach it, or call under "
+                         "torch.no_grad()")
+    if not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
+
 def _given_out(out, name: str, like):
-    """Strides of an output that the caller gives, with like's shape and type; what autograd saved of it before
-    counts as changed from here on."""
+    """Strides of an output that the caller gives, with like's shape and type."""
     if not isinstance(out, torch.Tensor) or out.shape != like.shape or out.dtype != like.dtype \
             or out.device != like.device:
         raise ValueError(f"{name} must be {like.dtype} {list(like.shape)} on {like.device}")
     _, ts, hs = _row_strides(out, name)
-    if not out.is_inference():
-        torch.autograd.graph.increment_version(out)
+    _overwritten(out, name)
     return ts, hs
-
-
-def _followed(t: torch.Tensor) -> bool:
-    """Whether autograd follows t: backwards, or forwards by a tangent (in whatever mode)."""
-    return t.requires_grad and torch.is_grad_enabled() or unpack_dual(t).tangent is not None
 
 
 def _launch(x, positions, rotary: Rotary, transpose: bool, out=None):
@@ -224,9 +232,9 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, *, transpos
     (int64 [tokens], or [axes, tokens] with the rotary's axes). head_dim is a multiple of 8, at least
     2 * rotary.pairs. Queries and keys that lie beside each other in a fused projection can be turned
     in one call. With ``transpose`` the transposed matrix (for factor 1 the turn back). ``out`` may be x
-    itself (in place); without it gradients flow to x, backwards only: a tangent of forward mode is refused.
-    As with any operator, a backward pass that is captured into a graph needs leaves that no eager graph
-    still holds."""
+    itself (in place) and must not be followed by autograd; without it gradients flow to x, backwards only: a
+    tangent of forward mode is refused. As with any operator, a backward pass that is captured into a graph
+    needs leaves that no eager graph still holds."""
     if isinstance(x, torch.Tensor) and _followed(x):
         if out is not None:
             raise ValueError("a call that needs gradients takes no out")

@@ -5,8 +5,8 @@ import torch
 import torch.autograd.forward_ad as forward_ad
 
 import rotary_ref as ref
-from scale_search_weights_amd import rotary
-from test_abi import G
+from scale_search_weights_amd import kvcache, rotary
+from test_abi import G, no_launch  # noqa: F401
 
 
 @pytest.fixture
@@ -63,3 +63,38 @@ def test_second_order(plain):
     y = rotary.rotate(x, pos, rot)
     gx, = torch.autograd.grad(y, x, u, create_graph=True)
     assert not gx.requires_grad and torch.equal(gx, rotary.rotate(u, pos, rot, transpose=True))
+
+
+def _graph_outputs(shape):
+    leaf = G(*shape).requires_grad_()
+    return {"a leaf": leaf, "a result": leaf * 2, "a view of a leaf": leaf[:, :, :]}
+
+
+@pytest.mark.parametrize("kind", ["a leaf", "a result", "a view of a leaf"])
+def test_outputs_in_a_graph_are_refused(no_launch, monkeypatch, kind):  # noqa: F811
+    """What is overwritten would keep the history of what it held."""
+    monkeypatch.setattr(kvcache, "_bound", None)
+    monkeypatch.setattr(rotary, "_bound", None)
+    _, pos, rot = make()
+    out = _graph_outputs((5, 2, 16))[kind]
+    x, slots, version = G(5, 2, 16), G(5, dtype=torch.int64), out._version
+    cache = kvcache.KVCache(G(4, 2, 16, 8, dtype=torch.uint8), G(4, 2, 16, 1, dtype=torch.uint8),
+                            G(4, 2, 16, 8, dtype=torch.uint8), G(4, 2, 16, 1, dtype=torch.uint8), G(2), G(2))
+    calls = [lambda: rotary.rotate(x, pos, rot, out=out),
+             lambda: kvcache.append(cache, x, x, slots, pos, rot, q=x, q_out=out),
+             lambda: kvcache.append(cache, x, x, slots, pos, rot, q=out, q_out=out)]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    assert out._version == version
+    with torch.no_grad():  # the caller's own doing, and what autograd saved of it counts as changed
+        assert rotary._given_out(out, "out", x) == (32, 16) and out._version == version + 1
+
+
+def test_outputs_with_a_tangent_are_refused(no_launch, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(rotary, "_bound", None)
+    _, pos, rot = make()
+    with forward_ad.dual_level(), torch.no_grad():
+        out = forward_ad.make_dual(G(5, 2, 16), G(5, 2, 16))
+        with pytest.raises(ValueError, match="gradient"):
+            rotary.rotate(G(5, 2, 16), pos, rot, out=out)
