@@ -89,6 +89,12 @@ class Rotary:
                           self.factor, int(self.adjacent))
         self._ref = ctypes.addressof(self._c)
 
+    def _of(self, inv_freq: torch.Tensor, axis: torch.Tensor | None) -> "Rotary":
+        """The Rotary with this one's tensors or copies of them."""
+        if inv_freq.data_ptr() == self._c.inv_freq and (axis is None or axis.data_ptr() == self._c.axis):
+            return self
+        return Rotary(inv_freq, axis, axes=self.axes, adjacent=self.adjacent, factor=self.factor)
+
     @classmethod
     def create(cls, rotary_dim: int, base: float = 10000.0, sections=None, *, adjacent: bool = False,
                factor: float = 1.0, device="cuda") -> "Rotary":
@@ -206,8 +212,8 @@ def _aligned(g):
 
 class _Turned(torch.autograd.Function):
     """y = R x; dx = R^T dy, which is differentiable in turn. The tensors that make R are inputs so that they
-    can be saved: a backward pass after one of them was changed is refused. Forward mode is not offered:
-    torch refuses a tangent here."""
+    can be saved: a backward pass after one of them was changed is refused or, where saved-tensor hooks kept
+    copies, takes those. Forward mode is not offered: torch refuses a tangent here."""
 
     @staticmethod
     def forward(ctx, x, positions, inv_freq, axis, rotary, transpose):
@@ -217,9 +223,10 @@ class _Turned(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, gy):
-        positions = ctx.saved_tensors[0]
+        positions, inv_freq, axis = ctx.saved_tensors
         turn = _turned if _followed(gy) else _launch
-        return turn(_aligned(gy), positions, ctx.rotary, not ctx.transpose), None, None, None, None, None
+        rotary = ctx.rotary._of(inv_freq, axis)
+        return turn(_aligned(gy), positions, rotary, not ctx.transpose), None, None, None, None, None
 
 
 def _turned(x, positions, rotary: Rotary, transpose: bool):

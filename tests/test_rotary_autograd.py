@@ -98,3 +98,25 @@ def test_outputs_with_a_tangent_are_refused(no_launch, monkeypatch):  # noqa: F8
         out = forward_ad.make_dual(G(5, 2, 16), G(5, 2, 16))
         with pytest.raises(ValueError, match="gradient"):
             rotary.rotate(G(5, 2, 16), pos, rot, out=out)
+
+
+def test_backward_takes_the_frequencies_that_forward_had(plain):
+    """Saved-tensor hooks (activations kept on the host, say) hand backward copies, and torch compares no versions
+    then: whatever the tensors hold meanwhile, the gradient is the transpose of the turn that was made."""
+    x, pos, _ = make()
+    w = 10.0 ** -torch.arange(8, dtype=torch.float64) + G(8, dtype=torch.float64)
+    axis, at = G(8, dtype=torch.int32), torch.stack((pos, 3 * pos + 1))
+    axis[::3] = 1
+    rot, before = (rotary.Rotary(a, b, axes=2, factor=1.25) for a, b in ((w, axis), (w.clone(), axis.clone())))
+    g = torch.randn_like(x)
+    want = rotary.rotate(g, at, rot, transpose=True)
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(), lambda t: t):
+        y = rotary.rotate(x.requires_grad_(), at, rot)
+    w += 1.0
+    axis[:] = 1 - axis
+    at += 5
+    v = g.clone().requires_grad_()
+    gx, = torch.autograd.grad(y, x, v, create_graph=True, retain_graph=True)
+    assert torch.equal(gx, want)
+    gv, = torch.autograd.grad(gx, v, g)
+    assert torch.equal(gv, rotary.rotate(g, at - 5, before))
