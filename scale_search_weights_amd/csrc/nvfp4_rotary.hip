@@ -263,13 +263,9 @@ static Items items_of(int n, const RowPlan &r, int64_t heads) {
   return {0, n, 0, r.heads, r.units, Div(r.units), Div(r.heads), Div(last)};
 }
 
-// f(adjacent, stream) with both as types. Rows are stored non-temporally where they pass the dies' L2, 32 MB in
-// all; fewer are left for whoever reads them next. us, non-temporal and ordinary, 32 bf16 heads of 128, three
-// inputs in turn: 16 MB 6.3, 6.7; 32 11.7, 11.6; 64 20.9, 22.8; 128 46.8, 41.2 (the ordinary ones find half of
-// it in the last cache); 256 92.4, 97.7. The append of 16384 tokens of 32 and 8 heads: 66, 69.
+// f(adjacent, stream) with both as types.
 template <typename F>
-static void with_flags(bool adjacent, int64_t bytes, F f) {
-  const bool stream = bytes > (32 << 20);
+static void with_flags(bool adjacent, bool stream, F f) {
   if (adjacent && stream) f(std::true_type{}, std::true_type{});
   else if (adjacent) f(std::true_type{}, std::false_type{});
   else if (stream) f(std::false_type{}, std::true_type{});
@@ -283,7 +279,7 @@ int launch_rotate(const Turn &turn, bool adjacent, bool transpose, const RowSpan
   const RotatePlan plan = rotate_plan(bf16, tokens, heads, head_dim, turn.pairs);
   const Rotate p = {turn, x.x, const_cast<void *>(out.x), x.ts, x.hs, out.ts, out.hs, transpose, Div(turn.pairs)};
   Items it = items_of(plan.tokens, plan.rows, heads);
-  with_flags(adjacent, tokens * heads * head_dim * (bf16 ? 2 : 4), [&](auto adj, auto stream) {
+  with_flags(adjacent, streams(bf16, tokens, heads, head_dim), [&](auto adj, auto stream) {
     each_chunks(tokens, plan.tokens, plan.rows.groups, [&](int64_t chunks, int64_t t0) {
       it.t0 = t0;
       const dim3 g((unsigned)chunks, (unsigned)plan.rows.groups), b(256);
@@ -427,7 +423,7 @@ int launch_kv_append(const nvfp4_kv_cache &c, const Turn &turn, bool adjacent, c
   p.kv_heads = (int)c.kv_heads, p.page_shift = __builtin_ctzll((unsigned long long)c.page_size);
   Items ikv = items_of(plan.tokens, plan.kv, c.kv_heads), iq = items_of(plan.tokens, plan.q, heads);
   const int64_t groups = 2 * plan.kv.groups + plan.q.groups;
-  with_flags(adjacent, tokens * heads * c.head_dim * (bf16 ? 2 : 4), [&](auto adj, auto stream) {
+  with_flags(adjacent, streams(bf16, tokens, heads, c.head_dim), [&](auto adj, auto stream) {
     each_chunks(tokens, plan.tokens, groups, [&](int64_t chunks, int64_t t0) {
       ikv.t0 = iq.t0 = t0;
       const dim3 g((unsigned)((chunks + 7) / 8 * 8 * groups)), b(256);

@@ -72,6 +72,14 @@ inline AppendPlan append_plan(bool bf16, int64_t tokens, int64_t heads, int64_t 
   return p;
 }
 
+// Whether the rows of a rotation, or of an append's queries, are stored non-temporally: where they pass the dies'
+// L2, 32 MB in all; fewer are left for whoever reads them next. us, non-temporal and ordinary, 32 bf16 heads of
+// 128, three inputs in turn: 16 MB 6.3, 6.7; 32 11.7, 11.6; 64 20.9, 22.8; 128 46.8, 41.2 (the ordinary ones find
+// half of it in the last cache); 256 92.4, 97.7. The append of 16384 tokens of 32 and 8 heads: 66, 69.
+inline bool streams(bool bf16, int64_t tokens, int64_t heads, int64_t head_dim) {
+  return tokens * heads * head_dim * (bf16 ? 2 : 4) > (32 << 20);
+}
+
 // f(chunks of this launch, the first one's first token), for all tokens in chunks of n: with `groups`
 // workgroups a chunk, of 256 threads, a launch stays under 2^32 threads.
 template <typename F>
