@@ -142,6 +142,18 @@ def _need(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must be contiguous")
 
 
+class _Fixed:
+    """A handle whose struct holds the addresses and sizes of its attributes: what is set stays."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} cannot be replaced: make another one")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{type(self).__name__}.{name} cannot be deleted")
+
+
 def _arg(t, name: str, like: torch.Tensor, dtype=None, numel: int | None = None,
          min_numel: int | None = None):
     """Another tensor argument, checked before anything is launched: a contiguous GPU

@@ -21,7 +21,7 @@ import torch
 from torch.autograd.forward_ad import unpack_dual
 
 from . import nvfp4
-from .nvfp4 import _I, _I64, _P, _check, _dt, _need
+from .nvfp4 import _I, _I64, _P, _check, _dt, _Fixed, _need
 
 MAX_HEAD_DIM = 1024
 MAX_PAIRS = 512
@@ -51,14 +51,14 @@ def lib():
     return _bound
 
 
-class Rotary:
+class Rotary(_Fixed):
     """How a head's first 2 * pairs channels turn; the others pass through.
 
     inv_freq [pairs] (fp64, on the GPU): pair i turns by position * inv_freq[i]; pairs is a multiple of
     4 (of 8 for ``kvcache.append``). axis [pairs] (int32, same GPU): the row of the positions that
     drives the pair, in any order; None: all on axis 0. A pair is channels i and i + pairs, or 2 i and
     2 i + 1 with ``adjacent``. Cosines and sines are multiplied by ``factor``. The tensors may be
-    changed between calls, not replaced."""
+    changed between calls; an attribute cannot be replaced."""
 
     def __init__(self, inv_freq: torch.Tensor, axis: torch.Tensor | None = None, *, axes: int = 1,
                  adjacent: bool = False, factor: float = 1.0):
