@@ -18,7 +18,7 @@ def test_attributes_stay(make):
     h = make()
     for name, value in list(vars(h).items()):
         with pytest.raises(AttributeError):
-            setattr(h, name, value.clone() if isinstance(value, torch.Tensor) else value)
+            setattr(h, name, value.clone() if isinstance(value, torch.Tensor) else object())
         with pytest.raises(AttributeError):
             delattr(h, name)
         assert getattr(h, name) is value
