@@ -20,7 +20,7 @@ import operator
 import torch
 
 from . import nvfp4
-from .nvfp4 import _I, _I64, _P, _SZ, _arg, _check, _dt, _need
+from .nvfp4 import _I, _I64, _P, _SZ, _arg, _check, _dt, _Fixed, _need
 from .rotary import Rotary, _given_out, _positions
 
 MAX_HEAD_DIM = 1024            # write, read
@@ -61,12 +61,13 @@ def lib():
     return _bound
 
 
-class KVCache:
+class KVCache(_Fixed):
     """One layer's cache. Tensors (contiguous, on one GPU):
     k_codes, v_codes [pages, kv_heads, page_size, head_dim / 2] uint8;
     k_scales, v_scales [pages, kv_heads, page_size, head_dim / 16] uint8;
     S_k, S_v [kv_heads] fp32, the tensor scale of each head (amax / 2688 of calibration data).
-    page_size is a power of two, 16 or more. Memory need not be initialised."""
+    page_size is a power of two, 16 or more. Memory need not be initialised. The tensors may be changed between
+    calls; an attribute cannot be replaced."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, S_k, S_v):
         _need(k_codes, "k_codes")

@@ -1,11 +1,11 @@
-"""Handles keep the memory and the sizes that the library was given: a Rotary's attributes cannot be replaced
-(no GPU needed)."""
+"""Handles keep the memory and the sizes that the library was given: attributes of a Rotary and of a KVCache
+cannot be replaced (no GPU needed)."""
 import copy
 
 import pytest
 import torch
 
-from scale_search_weights_amd import rotary
+from scale_search_weights_amd import kvcache, rotary
 from test_abi import G
 
 
@@ -13,7 +13,13 @@ def _rotary():
     return rotary.Rotary(G(32, dtype=torch.float64), G(32, dtype=torch.int32), axes=3)
 
 
-@pytest.mark.parametrize("make", [_rotary], ids=["Rotary"])
+def _cache():
+    u8 = torch.uint8
+    return kvcache.KVCache(G(4, 2, 16, 32, dtype=u8), G(4, 2, 16, 4, dtype=u8), G(4, 2, 16, 32, dtype=u8),
+                           G(4, 2, 16, 4, dtype=u8), G(2), G(2))
+
+
+@pytest.mark.parametrize("make", [_rotary, _cache], ids=["Rotary", "KVCache"])
 def test_attributes_stay(make):
     h = make()
     for name, value in list(vars(h).items()):
