@@ -21,7 +21,7 @@ import torch
 
 from . import nvfp4
 from .nvfp4 import _I, _I64, _P, _SZ, _arg, _check, _dt, _Fixed, _need
-from .rotary import Rotary, _given_out, _positions
+from .rotary import Rotary, _given_out, _overwritten, _positions
 
 MAX_HEAD_DIM = 1024            # write, read
 MAX_ATTENTION_HEAD_DIM = 256
@@ -263,7 +263,8 @@ def attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor | None 
 
     Returns out [tokens, heads, head_dim] in q's dtype (zeros for a query that sees nothing),
     and with return_lse also lse [tokens, heads] fp32 (the logarithm of the softmax sum; -inf for
-    such a query). `workspace` (uint8, attention_workspace_size bytes) saves an allocation."""
+    such a query). `out` (contiguous, of q's type and size) must not be followed by autograd. `workspace`
+    (uint8, attention_workspace_size bytes) saves an allocation."""
     dt, q_ts, q_hs = _rows(q, "q", cache, None)
     tokens, heads, hd = q.shape
     if hd > MAX_ATTENTION_HEAD_DIM:
@@ -314,6 +315,7 @@ def attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor | None 
         out = torch.empty(tokens, heads, hd, dtype=q.dtype, device=q.device)
     else:
         _arg(out, "out", q, q.dtype, numel=q.numel())
+        _overwritten(out, "out")
     lse = torch.empty(tokens, heads, dtype=torch.float32, device=q.device) if return_lse else None
     L = _bound or lib()
     if window is None:

@@ -120,3 +120,23 @@ def test_backward_takes_the_frequencies_that_forward_had(plain):
     assert torch.equal(gx, want)
     gv, = torch.autograd.grad(gx, v, g)
     assert torch.equal(gv, rotary.rotate(g, at - 5, before))
+
+
+@pytest.mark.parametrize("window", [None, 7])
+@pytest.mark.parametrize("kind", ["a leaf", "a result", "a view of a leaf"])
+def test_attention_refuses_outputs_in_a_graph(no_launch, monkeypatch, kind, window):  # noqa: F811
+    monkeypatch.setattr(kvcache, "_bound", None)
+    u8 = torch.uint8
+    cache = kvcache.KVCache(G(4, 2, 16, 8, dtype=u8), G(4, 2, 16, 1, dtype=u8), G(4, 2, 16, 8, dtype=u8),
+                            G(4, 2, 16, 1, dtype=u8), G(2), G(2))
+    out = _graph_outputs((5, 2, 16))[kind]
+
+    def call():
+        kvcache.attention(cache, G(5, 2, 16), G(5, 4, dtype=torch.int32), G(5, dtype=torch.int32), window=window, out=out)
+    version = out._version
+    with pytest.raises(ValueError, match="gradient"):
+        call()
+    assert out._version == version
+    with torch.no_grad(), pytest.raises(AssertionError, match="library"):  # goes on to the launch
+        call()
+    assert out._version == version + 1
