@@ -49,15 +49,6 @@ __device__ __forceinline__ void turn_of(double p, double w, double factor, float
 
 // ---------------------------------------------------------------- rows
 
-// Quotients of numbers below 2^16 by a divisor d up to 2^16, by one multiplication: m = floor(2^32 / d) + 1
-// exceeds 2^32 / d by at most 1, so n m / 2^32 exceeds n / d by less than 2^-16, less than 1 / d.
-struct Div {
-  int d;
-  unsigned m;
-  explicit Div(int d) : d(d), m(d == 1 ? 0 : (unsigned)((1ull << 32) / (unsigned)d + 1)) {}
-  __device__ __forceinline__ int of(int n) const { return m ? (int)__umulhi((unsigned)n, m) : n; }
-};
-
 // V values as they lie in memory, converted where they are used, so that a load can stay on its way.
 template <int DT, int V>
 struct Piece {

@@ -1,9 +1,25 @@
-// How the rotation and the append are split into workgroups: host code without HIP.
+// How the rotation and the append are split into workgroups, and the quotients by which a lane finds its item:
+// code that compiles without HIP.
 #pragma once
 
 #include <stdint.h>
 
 namespace nvfp4 {
+
+#if defined(__HIPCC__)
+#define NVFP4_HD __host__ __device__
+#else
+#define NVFP4_HD
+#endif
+
+// Quotients of numbers below 2^16 by a divisor d up to 2^16, by one multiplication: m = floor(2^32 / d) + 1
+// exceeds 2^32 / d by at most 1, so n m / 2^32 exceeds n / d by less than 2^-16, less than 1 / d.
+struct Div {
+  int d;
+  uint32_t m;
+  explicit Div(int d) : d(d), m(d == 1 ? 0 : (uint32_t)((1ull << 32) / (uint32_t)d + 1)) {}
+  inline NVFP4_HD int of(int n) const { return m ? (int)((uint64_t)(uint32_t)n * m >> 32) : n; }
+};
 
 constexpr int kTable = 2048;  // cosine and sine pairs of a workgroup: 16 KiB of LDS
 constexpr int kHeads = 64;    // key/value heads a workgroup takes at most (their scales are in LDS too)

@@ -21,3 +21,9 @@ extern "C" void rotary_append(const int64_t *c, int64_t *out) {
   for (const RowPlan &r : {p.kv, p.q}) *out++ = r.units, *out++ = r.heads, *out++ = r.groups;
   *out = streams(c[0] != 0, c[1], c[2], c[4]);
 }
+
+// the quotients of 0 .. 2^16 - 1 by d
+extern "C" void rotary_quotients(int d, int *out) {
+  const Div by(d);
+  for (int n = 0; n < 1 << 16; ++n) out[n] = by.of(n);
+}

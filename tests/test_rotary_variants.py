@@ -1,7 +1,11 @@
-"""The cases of rotary_cases.py reach every kernel variant and every shape of a split (no GPU needed)."""
+"""The cases of rotary_cases.py reach every kernel variant and every shape of a split, and the kernels' quotients
+are right (no GPU needed)."""
+import ctypes
 import itertools
 
-from rotary_cases import APPENDS, BF16, FP32, TURNS, append_plan, turn_plan
+import numpy as np
+
+from rotary_cases import APPENDS, BF16, FP32, TURNS, append_plan, lib, turn_plan
 
 
 def test_rotations_reach_every_variant():
@@ -26,3 +30,11 @@ def test_appends_reach_every_variant():
     ragged = {(c.dtype, c.adjacent) for c, p in plans if p.tokens > 1 and c.tokens % p.tokens}
     assert ragged == set(itertools.product([BF16, FP32], [False, True])), ragged
     assert any(p.tokens > 1 and p.kv.groups > 1 for _, p in plans) and any(c.heads == 0 for c in APPENDS)
+
+
+def test_the_kernels_quotients():
+    """The code that the kernels run, for every number below 2^16."""
+    n, out = np.arange(1 << 16), np.empty(1 << 16, np.int32)
+    for d in [*range(1, 1025), *range(1031, 1 << 16, 997), 4095, 4096, 4097, 32767, 32768, 65534, 65535, 65536]:
+        lib().rotary_quotients(d, out.ctypes.data_as(ctypes.POINTER(ctypes.c_int)))
+        assert np.array_equal(out, n // d), d
