@@ -386,7 +386,9 @@ __device__ __forceinline__ void append_items(const Append &p, const Items &it, i
 // one die: workgroups go to the 8 dies in turn. So those that quantise run beside those that only move
 // queries (16384 tokens of 32 and 8 heads of 128: 66 us, 74 with one role after the other). Six
 // workgroups a CU, 80 registers: 66 us, 68 with as many registers as it asks for, 83 with 64 (one role
-// after the other); fp32 needs 96.
+// after the other); fp32 needs 96. With pairs in halves that is five registers short: they are spilled around
+// the quantiser's exact search, which a block reaches only next to a rounding boundary, so scratch is
+// reserved but hardly touched.
 template <int DT, bool ADJACENT, bool STREAM>
 __global__ void __launch_bounds__(256, DT == NVFP4_DTYPE_F32 ? 5 : 6) k_kv_append(Append p, Items kv, Items q, int64_t tokens, int q_heads) {
   __shared__ __align__(16) float2 table[kTable + kTable / 8];

@@ -90,8 +90,11 @@ inline AppendPlan append_plan(bool bf16, int64_t tokens, int64_t heads, int64_t 
 
 // Whether the rows of a rotation, or of an append's queries, are stored non-temporally: where they pass the dies'
 // L2, 32 MB in all; fewer are left for whoever reads them next. us, non-temporal and ordinary, 32 bf16 heads of
-// 128, three inputs in turn: 16 MB 6.3, 6.7; 32 11.7, 11.6; 64 20.9, 22.8; 128 46.8, 41.2 (the ordinary ones find
-// half of it in the last cache); 256 92.4, 97.7. The append of 16384 tokens of 32 and 8 heads: 66, 69.
+// 128. On inputs and outputs that no cache holds: 16 MB 7.9, 8.0; 32 14.0, 14.0; 48 19.7, 21.6; 64 24.9, 25.9; 96
+// 35.7, 38.3; 128 47.3, 49.1; 256 92.6, 95.0; 512 187.2, 186.9. Two of each in turn: 64 21.0, 22.1; 96 30.4, 38.2;
+// 128 40.7, 48.4 (ordinary rows put inputs out of the last cache). Between a kernel that writes the input and one
+// that reads the output, all three: 16 MB 20.5, 19.4; 32 34.4, 32.9; 48 48.0, 46.2; 64 62.5, 60.6; 96 95.6, 100.7;
+// 128 125.9, 133.5; 256 279, 271. The append of 16384 tokens of 32 and 8 heads: 66, 69.
 inline bool streams(bool bf16, int64_t tokens, int64_t heads, int64_t head_dim) {
   return tokens * heads * head_dim * (bf16 ? 2 : 4) > (32 << 20);
 }
