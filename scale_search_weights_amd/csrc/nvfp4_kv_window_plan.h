@@ -44,7 +44,10 @@ inline WindowPlan window_rows_plan(const KvAttention &a, int64_t window, int64_t
 
 // What workgroups of k_kv_attn_tile take, us, with k of them for a CU: start + more k to begin and end, and for 64
 // tokens `alone` and `beside` for each other one of up to `fit` that share the CU; what is beyond them
-// takes turns. Fitted to 128 to 1024 workgroups on windows of 512 and 2048 tokens, within a tenth.
+// takes turns. Fitted to 128 to 1024 workgroups on windows of 512 and 2048 tokens, heads of 64, 128 and 256. Measured
+// again in short runs, which clock higher, the estimates are 1 to 30% high, by much the same for all kernels of a
+// type and head, for heads of 80, 96 and 160 too; two stand out: fp32 heads of 256, 10 to 22% low (there is one tile
+// to choose), and fp32 heads of 64 on four waves, up to 40% high where more than three share a CU.
 struct TileCost {
   double start, more, alone, beside;
   int fit;
@@ -69,6 +72,8 @@ inline double tile_time(const TileCost &c, double k, double steps) {
 // MB of partial sums. Estimated and measured, eight key/value heads of 128, four query heads each: 2 x 2048
 // queries, window 1024: 256 rows a tile 97, 92; 128 rows 108, 99; 64 rows 144, 141. 512 queries, window 1024:
 // 64 rows whole 34, 30, in two pieces 39, 36. 8 x 64, window 512: 64 rows 21, 19; 256 rows 33, 30.
+// Of 80 calls (eight sizes, heads of 64 to 256, both types) 72 take at most 2% more than the best of all tiles in
+// one, two and four pieces, the others 6 to 20%: 100 and 512 queries, which more pieces would serve better.
 inline WindowPlan window_tile_plan(const KvAttention &a, int64_t window, int64_t sinks) {
   WindowPlan best = {};
   double least = INFINITY;
