@@ -143,11 +143,11 @@ def _need(t: torch.Tensor, name: str):
 
 
 class _Fixed:
-    """A handle whose struct holds the addresses and sizes of its attributes: what is set stays. (A change in
-    place, `handle.tensor += 1`, sets the same object again.)"""
+    """A handle whose struct holds the addresses and sizes of its public attributes: what is set stays. (A change
+    in place, `handle.tensor += 1`, sets the same object again.)"""
 
     def __setattr__(self, name, value):
-        if name in self.__dict__ and self.__dict__[name] is not value:
+        if name[0] != "_" and name in self.__dict__ and self.__dict__[name] is not value:
             raise AttributeError(f"{type(self).__name__}.{name} cannot be replaced: make another one")
         super().__setattr__(name, value)
 
